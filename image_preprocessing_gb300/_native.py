@@ -59,6 +59,7 @@ _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 _f = ctypes.c_float
 _fp = ctypes.POINTER(ctypes.c_float)
 _u64 = ctypes.c_uint64
@@ -107,6 +108,13 @@ _SIGNATURES = {
     "tr_stage_destroy": (_i, [_vp]),
     "tr_ts_sync": (_i, [_vp, _i]),
     "tr_ts_destroy": (_i, [_vp]),
+    "tr_rms_norm": (_i, [_vp] * 6 + [_ll] * 6 + [_i, _i, _f, _vp]),
+    "tr_rms_norm_backward_workspace_bytes": (ctypes.c_size_t, [_ll, _ll]),
+    "tr_rms_norm_backward": (_i, [_vp] * 6 + [_ll] * 6 + [_i, _f, _vp, _vp]),
+    "tr_quantize_rows": (_i, [_vp] * 3 + [_ll] * 4 + [_i, _vp]),
+    "tr_dequantize_rows": (_i, [_vp] * 3 + [_ll] * 4 + [_i, _vp]),
+    "tr_int8_matmul_workspace_bytes": (ctypes.c_size_t, [_ll] * 3),
+    "tr_int8_matmul": (_i, [_vp] * 6 + [_ll] * 6 + [_i, _vp, _vp]),
     "tr_device_status": (_i, [ctypes.POINTER(_i), _i]),
     "tr_launch_count": (_u64, []),
     "tr_tune_tiled": (_i, [_i, _i, _i, _i]),

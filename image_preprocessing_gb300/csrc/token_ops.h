@@ -1,0 +1,79 @@
+// Internal declarations of the token-row operators (the C ABI is
+// include/tr_token_ops.h): arguments after the host checks, and launchers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.h"
+#include "tr_token_ops.h"
+
+namespace trfn {
+
+// Norm or quantisation of rows; what == kQuantize has no residual, weight or eps.
+enum RowWhat { kNorm, kNormQ8, kQuantize };
+struct RowArgs {
+    const void* x;
+    const void* residual;      // or null
+    const float* weight;       // or null
+    void* out;
+    void* residual_out;        // or null
+    float* scale;
+    long long rows, x_stride, residual_stride, out_stride, residual_out_stride;
+    int cols;
+    float eps;
+    int dtype;
+    RowWhat what;
+    void* stream;
+};
+int launch_rows(const RowArgs& a);
+
+struct RowGradArgs {
+    const void* dy;
+    const void* h;
+    const float* weight;       // or null
+    const void* dresidual;     // or null
+    void* dx;
+    float* dweight;            // or null
+    float* partial;            // workspace for a dweight
+    long long rows, dy_stride, h_stride, dresidual_stride, dx_stride;
+    int cols;
+    float eps;
+    int dtype;
+    void* stream;
+};
+int launch_row_grad(const RowGradArgs& a);
+// CTAs of the gradient kernel, each with one partial dweight row.
+int row_grad_parts(long long rows, long long cols);
+
+struct DequantArgs {
+    const int8_t* q;
+    const float* scale;
+    void* out;
+    long long rows, q_stride, out_stride;
+    int cols;
+    int dtype;
+    void* stream;
+};
+int launch_dequant(const DequantArgs& a);
+
+struct MatmulArgs {
+    const int8_t* x;
+    const float* x_scale;
+    const int8_t* w;
+    const float* w_scale;
+    const float* bias;         // or null
+    void* y;
+    int M, N, K;
+    long long x_stride, w_stride, y_stride;
+    int out_dtype;
+    void* workspace;
+    void* stream;
+};
+int launch_int8_matmul(const MatmulArgs& a);
+size_t int8_matmul_workspace(long long M, long long N, long long K);
+
+// cudaGetLastError() after a launch as a tr_status; counts the launch.
+int launched(const char* what);
+
+}  // namespace trfn
