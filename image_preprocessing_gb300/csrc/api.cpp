@@ -11,6 +11,7 @@
 
 #include "internal.h"
 #include "stream_guard.h"
+#include "token_ops.h"
 
 namespace trfn {
 
@@ -437,7 +438,11 @@ int tr_validate_aug_params(const tr_aug_param* p, int N, int H, int W, int* bad_
 
 int tr_device_status(int* flags, int clear) {
     if (flags == nullptr) return TR_ERR_INVALID_ARGUMENT;
-    return read_device_status(flags, clear != 0);
+    int norm = 0, product = 0;
+    int rc = read_device_status(&norm, clear != 0);
+    if (rc == TR_OK) rc = read_gemm_status(&product, clear != 0);
+    if (rc == TR_OK) *flags = norm | product;
+    return rc;
 }
 
 uint64_t tr_launch_count(void) { return launch_count(); }

@@ -22,6 +22,7 @@ int launched(const char* what) {
 namespace {
 
 constexpr long long kMaxRows = 2147483647LL;
+constexpr long long kMaxProductRows = TR_MAX_INT8_ROWS;   // row numbers of whole tiles stay below 2^31
 constexpr long long kMaxStride = 1LL << 40;
 
 int elem_bytes(int dtype) {
@@ -211,7 +212,7 @@ int tr_dequantize_rows(const int8_t* q, const float* scale, void* out, long long
 }
 
 size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K) {
-    if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > TR_MAX_INT8_K) return 0;
+    if (M < 1 || N < 1 || K < 1 || M > kMaxProductRows || N > kMaxProductRows || K > TR_MAX_INT8_K) return 0;
     return int8_matmul_workspace(M, N, K);
 }
 
@@ -219,7 +220,7 @@ int tr_int8_matmul(const int8_t* x, const float* x_scale, const int8_t* w, const
                    const float* bias, void* y, long long M, long long N, long long K, long long x_stride,
                    long long w_stride, long long y_stride, int out_dtype, void* workspace, void* stream) {
     if (!is_float(out_dtype) || M < 0 || N < 0 || K < 0) return TR_ERR_INVALID_ARGUMENT;
-    if (M > kMaxRows || N > kMaxRows || K > TR_MAX_INT8_K) return TR_ERR_NOT_SUPPORTED;
+    if (M > kMaxProductRows || N > kMaxProductRows || K > TR_MAX_INT8_K) return TR_ERR_NOT_SUPPORTED;
     if (M == 0 || N == 0) return TR_OK;
     const Mat mx{x, M, K, row_stride(M, K, x_stride), 1};
     const Mat mw{w, N, K, row_stride(N, K, w_stride), 1};

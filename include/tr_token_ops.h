@@ -48,6 +48,8 @@ typedef enum tr_elem {
  * above), and longest sum of tr_int8_matmul: 2^14 * 131071 < 2^31.           */
 #define TR_MAX_ROW 32768
 #define TR_MAX_INT8_K 131071
+/* Most tokens or channels of tr_int8_matmul.                                */
+#define TR_MAX_INT8_ROWS 2147479552
 
 /* 8-bit rows.  With a = max_c |v_c| of a row v:
  *     scale = a / 127,   q_c = v_c * (127 / a) rounded to nearest (ties to even),
@@ -118,7 +120,7 @@ size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K);
  *            not initialised; NULL where that is 0.
  * The sum is exact in integers; it is rounded to binary32 once, scaled, and
  * rounded to out_dtype.  K = 0 gives the bias.
- * TR_ERR_NOT_SUPPORTED for K > TR_MAX_INT8_K or M, N > 2^31 - 1.            */
+ * TR_ERR_NOT_SUPPORTED for K > TR_MAX_INT8_K or M, N > TR_MAX_INT8_ROWS.    */
 int tr_int8_matmul(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
                    const float* bias, void* y, long long M, long long N, long long K, long long x_stride,
                    long long w_stride, long long y_stride, int out_dtype, void* workspace, void* stream);

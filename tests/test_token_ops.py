@@ -355,7 +355,8 @@ def test_int8_matmul_tokens(M, dtype):
 
 @gpu
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 5000, 2048), (48, 1000, 8192), (300, 384, 20000), (1024, 1024, 768),
-                                   (2049, 515, 640), (4000, 1536, 1023), (12544, 256, 128)])
+                                   (2049, 515, 640), (4000, 1536, 1023), (12544, 256, 128), (2049, 1539, 640), (1100, 4097, 333), (515, 4096, 1040), (20000, 1000, 65),
+                                   (8192, 300, 2100), (700, 9000, 4096)])
 def test_int8_matmul_larger(M, N, K):
     g = torch.Generator(device="cuda").manual_seed(M + N + K)
     check_product(any_int8(g, M, K), any_int8(g, N, K), torch.float32, True)
@@ -451,11 +452,20 @@ def test_rows_far_apart():
 
 
 @gpu
+def test_no_wait_ran_out():
+    """The product's pipelines report a wait that ran out in the status word."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for _ in range(20):
+        check_product(any_int8(g, 3000, 1024), any_int8(g, 2048, 1024), torch.bfloat16, True)
+    assert trfn.tr_device_status() == 0
+
+
+@gpu
 def test_other_stream_and_graph():
     """The calls run on the stream they are given, and can be captured."""
     g = torch.Generator(device="cuda").manual_seed(3)
     side = torch.cuda.Stream()
-    for M in (4, 150, 900):
+    for M in (4, 150, 9000):
         x = torch.randn(M, 512, generator=g, device="cuda").half()
         w = any_int8(g, 384, 512)
         sw = torch.rand(384, generator=g, device="cuda")
