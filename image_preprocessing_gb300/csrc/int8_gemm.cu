@@ -13,7 +13,12 @@
 // even CTA) issues the products, eight warps read the sums: sums of 1024
 // products are read into integer registers while the other half of TMEM
 // takes the next 1024, so the reading is hidden.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <atomic>
+#include <climits>
+#include <mutex>
 
 #include "int8_parts.h"
 #include "token_ops.h"
@@ -61,11 +66,17 @@ __device__ __forceinline__ void bar_arrive_even(uint32_t bar) {
         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
         : "memory");
 }
+// This CTA's address `bar` in the even CTA.
+__device__ __forceinline__ uint32_t in_even(uint32_t bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
+    return a;
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -75,11 +86,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Waits for the phase with this parity; false after about a second, or as soon
 // as another thread of the CTA gave up.
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* given_up) {
-    const uint64_t t0 = now_ns();
-    for (uint32_t i = 0; i < (1u << 28); ++i) {
+    uint64_t t0 = 0;   // reading the timer takes longer than a product: not before the wait is a long one
+    for (uint32_t i = 1; i < (1u << 28); ++i) {
         if (bar_try(bar, parity)) return true;
-        if (*given_up) return false;
-        if ((i & 63u) == 63u && now_ns() - t0 > kWaitLimitNs) break;
+        if ((i & 255u) == 0) {
+            if (*given_up) return false;
+            if (t0 == 0) t0 = now_ns();
+            else if (now_ns() - t0 > kWaitLimitNs) break;
+        }
     }
     *given_up = 1;
     atomicOr(&g_gemm_status, kStatusTimeout);
@@ -88,10 +102,14 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* given_up) {
     return bar_try(bar, parity) || bar_wait_slow(bar, parity, given_up);
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+// Box of a tensor map at row `row`; the bytes count on `bar`, a barrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -116,15 +134,25 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
+// Barrier of the eight epilogue warps; whether any of them passed a true flag.
+__device__ __forceinline__ bool epilogue_barrier(bool flag) {
+    uint32_t any;
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "{\n\t.reg .pred q, p;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 256, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)flag)
+        : "memory");
+    return any != 0;
+}
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -170,8 +198,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
 // --------------------------------------------------------------- product ---
 
 struct GemmParams {
-    const uint8_t* xh;        // blocks of x, then of w
-    const uint8_t* wh;
+    CUtensorMap x, w;         // the copies: all block rows of 64 values, boxes of 128 and BN/2 rows
     const float* x_scale;
     const float* w_scale;
     const float* bias;
@@ -180,25 +207,30 @@ struct GemmParams {
     int M, N, k_blocks, m_tiles, n_tiles, wide;   // wide: rows of y take 16-byte stores
 };
 
+// Shared memory: the ring, 2 KB for each epilogue warp, (scale, bias) of two
+// tiles' channels.
 template <int BN> constexpr int kStageBytes = kBlockBytes + BN / 2 * 128;
 template <int BN> constexpr int kStages = BN == 256 ? 6 : 8;
-template <int BN> constexpr int kSmemBytes = kStages<BN> * kStageBytes<BN> + 1024;
+constexpr int kPassBytes = 64;   // of a row of y that pass through a warp's 2 KB at a time
+template <int BN> constexpr int kSmemBytes =
+    1024 + kStages<BN> * kStageBytes<BN> + kEpilogueWarps * 32 * kPassBytes + 2 * BN * 8;
 
-template <typename E, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const GemmParams p) {
+// ONE: K <= 1024, one sum in TMEM for each value of y.
+template <typename E, int BN, bool ONE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
     constexpr int ST = kStages<BN>;
     extern __shared__ uint8_t smem_raw[];
-    // full[ST] peer[ST] empty[ST] sums_full[2] sums_empty[2]
-    __shared__ __align__(8) uint64_t bars[3 * ST + 4];
+    // full[ST] empty[ST] sums_full[2] sums_empty[2]
+    __shared__ __align__(8) uint64_t bars[2 * ST + 4];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int given_up;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* const base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t ring = smem_u32(base);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto peer = [&](int s) { return bar0 + 8u * (ST + s); };
-    auto empty = [&](int s) { return bar0 + 8u * (2 * ST + s); };
-    auto sums_full = [&](int s) { return bar0 + 8u * (3 * ST + s); };
-    auto sums_empty = [&](int s) { return bar0 + 8u * (3 * ST + 2 + s); };
+    auto empty = [&](int s) { return bar0 + 8u * (ST + s); };
+    auto sums_full = [&](int s) { return bar0 + 8u * (2 * ST + s); };
+    auto sums_empty = [&](int s) { return bar0 + 8u * (2 * ST + 2 + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
@@ -206,7 +238,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         given_up = 0;
         for (int s = 0; s < ST; ++s) {
             bar_init(full(s), 1);
-            bar_init(peer(s), 1);
             bar_init(empty(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -229,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
 
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = p.m_tiles * p.n_tiles;
-    const int parts = (p.k_blocks + kExactBlocks - 1) / kExactBlocks;
+    const int parts = ONE ? 1 : (p.k_blocks + kExactBlocks - 1) / kExactBlocks;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -238,27 +269,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             uint32_t phase = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                const long long mt = tile / p.n_tiles, nt = tile % p.n_tiles;
-                const uint8_t* xb = p.xh + (mt * 2 + rank) * p.k_blocks * kBlockBytes;
+                const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
+                const int xb = (mt * 2 + (int)rank) * p.k_blocks;
                 // this CTA's BN/2 channels: a block, or half of one
-                const long long ch = nt * BN + (long long)rank * (BN / 2);
-                const uint8_t* wb = p.wh + (ch >> 7) * p.k_blocks * kBlockBytes + (ch & 127) * 128;
+                const int ch = nt * BN + (int)rank * (BN / 2);
+                const int wb = (ch >> 7) * p.k_blocks, sub = ch & 127;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!bar_wait(empty(s), phase ^ 1u, &given_up)) { ok = false; break; }
                     const uint32_t at = ring + s * kStageBytes<BN>;
-                    bar_expect(full(s), kStageBytes<BN>);
-                    bulk_load(at, xb + (long long)kb * kBlockBytes, kBlockBytes, full(s));
-                    bulk_load(at + kBlockBytes, wb + (long long)kb * kBlockBytes, BN / 2 * 128, full(s));
+                    // both CTAs' bytes count on the even one's barrier
+                    if (rank == 0) bar_expect(full(s), 2 * kStageBytes<BN>);
+                    tensor_load(at, &p.x, (xb + kb) * kBlockRows, in_even(full(s)));
+                    tensor_load(at + kBlockBytes, &p.w, (wb + kb) * kBlockRows + sub, in_even(full(s)));
                     issued = issued < ST ? issued + 1 : ST;
                     if (++s == ST) { s = 0; phase ^= 1u; }
                 }
             }
-            // copies in flight land before the CTA ends, whatever became of the others
-            for (int i = 0; i < issued; ++i) {
-                s = s == 0 ? ST - 1 : s - 1;
-                if (s == ST - 1) phase ^= 1u;
-                for (int n = 0; n < (1 << 20) && !bar_try(full(s), phase); ++n) {}
-            }
+            // copies in flight land before the pair ends, whatever became of the others (in a run that gave
+            // up, the odd CTA's may be counted nowhere: it leaves them a thousand times their duration)
+            if (rank != 0 && !ok) __nanosleep(1000000);
+            if (rank == 0)
+                for (int i = 0; i < issued; ++i) {
+                    s = s == 0 ? ST - 1 : s - 1;
+                    if (s == ST - 1) phase ^= 1u;
+                    for (int n = 0; n < (1 << 20) && !bar_try(full(s), phase); ++n) {}
+                }
         }
     } else if (warp == 1 && rank == 0) {
         if (lane == 0) {
@@ -274,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                     const uint32_t d = tmem + half * BN;
                     const int kb0 = part * kExactBlocks, kb1 = min(p.k_blocks, kb0 + kExactBlocks);
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        ok = bar_wait(full(s), phase, &given_up) && bar_wait(peer(s), phase, &given_up);
+                        ok = bar_wait(full(s), phase, &given_up);
                         if (!ok) break;
                         tmem_fence_after();
                         const uint32_t at = ring + s * kStageBytes<BN>;
@@ -294,42 +329,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             if (pair < tiles)
                 for (int n = 0; n < (1 << 20) && !bar_try(sums_full(last), last_phase); ++n) {}
         }
-    } else if (warp == 1) {
-        if (lane == 0) {   // tells the even CTA that this one's half of a stage has landed
-            int s = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs)
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    ok = bar_wait(full(s), phase, &given_up);
-                    if (!ok) break;
-                    bar_arrive_even(peer(s));
-                    if (++s == ST) { s = 0; phase ^= 1u; }
-                }
-        }
     } else if (warp >= 4) {
-        constexpr int W = BN / 2;                                  // channels of a warp
-        const int quarter = warp & 3, col0 = (warp - 4) / 4 * W;
-        int half = 0;
+        constexpr int W = BN / 2;                      // channels of a warp
+        constexpr int V = 16 / sizeof(E), C = kPassBytes / sizeof(E);   // channels of 16 bytes, of a pass
+        const int quarter = warp & 3, col0 = (warp - 4) / 4 * W, me = threadIdx.x - 128;
+        uint8_t* const pass = base + ST * kStageBytes<BN> + (warp - 4) * 32 * kPassBytes;
+        float2* const channel = reinterpret_cast<float2*>(base + ST * kStageBytes<BN> + kEpilogueWarps * 32 * kPassBytes);
+        int half = 0, buf = 0;
         uint32_t half_phase = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        for (int tile = pair; tile < tiles; tile += pairs) {
             const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
-            int acc[W];
-            for (int part = 0; part < parts; ++part) {
-                ok = bar_wait(sums_full(half), half_phase, &given_up);
-                ok = __all_sync(0xffffffffu, ok);
+            // scale and bias of the tile's channels; the other buffer may still be in use
+            buf ^= 1;
+            if (me < BN) {
+                const int n = nt * BN + me;
+                channel[buf * BN + me] = n < p.N ? make_float2(p.w_scale[n], p.bias != nullptr ? p.bias[n] : 0.0f)
+                                                 : make_float2(0.0f, 0.0f);
+            }
+            const int m0 = mt * 256 + (int)rank * 128 + quarter * 32;
+            const float sx = m0 + lane < p.M ? p.x_scale[m0 + lane] : 0.0f;
+            if (epilogue_barrier(!ok)) break;
+            int acc[ONE ? 1 : W];
+            for (int part = 0; part < parts - 1; ++part) {
+                ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
+                if constexpr (!ONE) {
 #pragma unroll
-                for (int c = 0; c < W; c += 32) {
-                    uint32_t v[32];
-                    tmem_load32(at + c, v);
+                    for (int c = 0; c < W; c += 16) {
+                        uint32_t v[16];
+                        tmem_load16(at + c, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int sum = __float2int_rn(__uint_as_float(v[i]));
-                        acc[c + i] = part == 0 ? sum : acc[c + i] + sum;
+                        for (int i = 0; i < 16; ++i) {
+                            const int sum = __float2int_rn(__uint_as_float(v[i]));
+                            acc[c + i] = part == 0 ? sum : acc[c + i] + sum;
+                        }
                     }
                 }
                 tmem_fence_before();
@@ -337,34 +373,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 if (lane == 0) bar_arrive_even(sums_empty(half));
                 if (++half == 2) { half = 0; half_phase ^= 1u; }
             }
-            if (!ok) break;
-            const long long m = (long long)mt * 256 + rank * 128 + quarter * 32 + lane;
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up));
+            if (!ok) continue;   // to the barrier, where all eight warps leave together
+            tmem_fence_after();
+            const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
             const int n0 = nt * BN + col0;
-            if (m < p.M) {
-                const float sx = p.x_scale[m];
-                E* y = static_cast<E*>(p.y) + m * p.y_stride + n0;
-                constexpr int V = 16 / sizeof(E);
 #pragma unroll
-                for (int c = 0; c < W; c += V) {
+            for (int c = 0; c < W; c += 16) {
+                uint32_t v[16];
+                tmem_load16(at + c, v);
+                if (c + 16 == W) {   // TMEM is read: the next sums may go there
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_even(sums_empty(half));
+                    if (++half == 2) { half = 0; half_phase ^= 1u; }
+                }
+                // through the warp's 2 KB, 64 bytes of each row at a time, so that rows of y are written in
+                // 64-byte runs; piece q of row r lies at q ^ (r >> 1 & 3): no bank conflicts
+#pragma unroll
+                for (int i = 0; i < 16; i += V) {
                     union { uint4 word; E e[V]; } o;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int n = n0 + c + i;
-                        float v = 0.0f;
-                        if (n < p.N) {
-                            v = (float)acc[c + i] * sx * p.w_scale[n];
-                            if (p.bias != nullptr) v += p.bias[n];
-                        }
-                        o.e[i] = out_value<E>(v);
-                    }
-                    if (p.wide && n0 + c + V <= p.N) {
-                        *reinterpret_cast<uint4*>(y + c) = o.word;
-                    } else {
+                    for (int j = 0; j < V; j += 2) {
+                        const float4 two = *reinterpret_cast<const float4*>(&channel[buf * BN + col0 + c + i + j]);
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (n0 + c + i < p.N) y[c + i] = o.e[i];
+                        for (int h = 0; h < 2; ++h) {
+                            float sum = __uint_as_float(v[i + j + h]);
+                            if constexpr (!ONE)
+                                if (parts > 1) sum = (float)(acc[c + i + j + h] + __float2int_rn(sum));
+                            o.e[j + h] = out_value<E>(sum * sx * (h ? two.z : two.x) + (h ? two.w : two.y));
+                        }
+                    }
+                    const int q = (c + i) % C / V;
+                    *reinterpret_cast<uint4*>(pass + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16) = o.word;
+                }
+                if ((c + 16) % C != 0) continue;
+                __syncwarp();
+                const int n = n0 + c + 16 - C;
+                E* y = static_cast<E*>(p.y) + (long long)m0 * p.y_stride + n;
+                if (p.wide && n + C <= p.N) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2), q = lane & 3;
+                        const uint4 o = *reinterpret_cast<const uint4*>(pass + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
+                        if (m0 + r < p.M) *reinterpret_cast<uint4*>(y + r * p.y_stride + q * V) = o;
+                    }
+                } else {
+                    constexpr int R = 32 / C;   // rows of C values at a time
+                    for (int r = lane / C; r < 32; r += R) {
+                        const int e = lane % C, q = e / V;
+                        const E o = *(reinterpret_cast<const E*>(pass + r * 64 + ((q ^ (r >> 1)) & 3) * 16) + e % V);
+                        if (m0 + r < p.M && n + e < p.N) y[r * p.y_stride + e] = o;
                     }
                 }
+                __syncwarp();
             }
         }
     }
@@ -379,11 +441,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
 
 int pieces_of(int v, int of) { return (int)(((long long)v + of - 1) / of); }
 
-template <typename E, int BN>
-int start_gemm(const GemmParams& q, cudaStream_t st) {
+// `rows` block rows of 64 binary16 at `p`, boxes of `box` of them.
+int block_map(CUtensorMap* map, void* p, long long rows, int box) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (encode == nullptr) {
+        set_last_error("cuTensorMapEncodeTiled unavailable", (int)cudaErrorNotSupported);
+        return TR_ERR_CUDA;
+    }
+    const cuuint64_t dims[2] = {kBlockK, (cuuint64_t)rows}, strides[1] = {kBlockK * 2};
+    const cuuint32_t boxes[2] = {kBlockK, (cuuint32_t)box}, elem[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, dims, strides, boxes, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_last_error("cuTensorMapEncodeTiled", (int)cudaErrorInvalidValue);
+        return TR_ERR_CUDA;
+    }
+    return TR_OK;
+}
+
+struct Copies {
+    void* xh;
+    void* wh;
+    long long x_rows, w_rows;   // block rows: 64 values each
+};
+
+template <typename E, int BN, bool ONE>
+int start_gemm(const GemmParams& q, const Copies& c, cudaStream_t st) {
     GemmParams p = q;
     p.m_tiles = pieces_of(p.M, 256);
     p.n_tiles = pieces_of(p.N, BN);
+    int rc = block_map(&p.x, c.xh, c.x_rows, kBlockRows);
+    if (rc == TR_OK) rc = block_map(&p.w, c.wh, c.w_rows, BN / 2);
+    if (rc != TR_OK) return rc;
     const long long tiles = (long long)p.m_tiles * p.n_tiles;
     if (tiles > (1LL << 30)) return TR_ERR_NOT_SUPPORTED;
     cudaLaunchConfig_t cfg{};
@@ -395,8 +493,8 @@ int start_gemm(const GemmParams& q, cudaStream_t st) {
     int n = pairs.load(std::memory_order_relaxed);
     if (n == 0) {
         cfg.gridDim = dim3(2);
-        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<E, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<BN>);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel<E, BN>, &cfg);
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<E, BN, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<BN>);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel<E, BN, ONE>, &cfg);
         if (e != cudaSuccess || n < 1) {
             set_last_error("int8 product kernel set-up", (int)e);
             return TR_ERR_CUDA;
@@ -409,7 +507,7 @@ int start_gemm(const GemmParams& q, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<E, BN>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<E, BN, ONE>, p);
     if (e != cudaSuccess) {
         set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
         return TR_ERR_CUDA;
@@ -417,11 +515,16 @@ int start_gemm(const GemmParams& q, cudaStream_t st) {
     return launched("int8 product kernel");
 }
 
+template <typename E, int BN>
+int pick_parts(const GemmParams& p, const Copies& c, cudaStream_t st) {
+    return p.k_blocks <= kExactBlocks ? start_gemm<E, BN, true>(p, c, st) : start_gemm<E, BN, false>(p, c, st);
+}
+
 template <typename E>
-int pick_gemm(const GemmParams& p, cudaStream_t st) {
+int pick_gemm(const GemmParams& p, const Copies& c, cudaStream_t st) {
     // the narrower tile where the wide one leaves pairs of SMs without any
     const long long wide = (long long)pieces_of(p.M, 256) * pieces_of(p.N, 256);
-    return wide >= 76 ? start_gemm<E, 256>(p, st) : start_gemm<E, 128>(p, st);
+    return wide >= 76 ? pick_parts<E, 256>(p, c, st) : pick_parts<E, 128>(p, c, st);
 }
 
 }  // namespace
@@ -440,6 +543,7 @@ int launch_int8_gemm(const MatmulArgs& a) {
     c.w = ByteRows{a.w, a.w_stride, a.w + (a.N - 1) * a.w_stride + a.K, a.N, a.K};
     c.x_pieces = (long long)pieces_of(a.M, 256) * 2 * kb * (kBlockBytes / 32);
     c.w_pieces = (long long)pieces_of(a.N, 256) * 2 * kb * (kBlockBytes / 32);
+    if (c.x_pieces / 4 > INT_MAX || c.w_pieces / 4 > INT_MAX) return TR_ERR_NOT_SUPPORTED;   // rows of a tensor map
     c.xh = static_cast<uint4*>(a.workspace);
     c.wh = c.xh + c.x_pieces * 2;
     c.k_blocks = kb;
@@ -451,8 +555,7 @@ int launch_int8_gemm(const MatmulArgs& a) {
     const int rc = launched("int8 copy kernel");
     if (rc != TR_OK) return rc;
     GemmParams p{};
-    p.xh = reinterpret_cast<const uint8_t*>(c.xh);
-    p.wh = reinterpret_cast<const uint8_t*>(c.wh);
+    const Copies copies{c.xh, c.wh, c.x_pieces / 4, c.w_pieces / 4};
     p.x_scale = a.x_scale;
     p.w_scale = a.w_scale;
     p.bias = a.bias;
@@ -461,9 +564,9 @@ int launch_int8_gemm(const MatmulArgs& a) {
     p.M = a.M; p.N = a.N; p.k_blocks = kb;
     const int es = a.out_dtype == TR_ELEM_F32 ? 4 : 2;
     p.wide = (uintptr_t)a.y % 16 == 0 && (a.y_stride * es) % 16 == 0;
-    if (a.out_dtype == TR_ELEM_F32) return pick_gemm<float>(p, st);
-    if (a.out_dtype == TR_ELEM_F16) return pick_gemm<__half>(p, st);
-    return pick_gemm<__nv_bfloat16>(p, st);
+    if (a.out_dtype == TR_ELEM_F32) return pick_gemm<float>(p, copies, st);
+    if (a.out_dtype == TR_ELEM_F16) return pick_gemm<__half>(p, copies, st);
+    return pick_gemm<__nv_bfloat16>(p, copies, st);
 }
 
 int read_gemm_status(int* flags, bool clear) {
