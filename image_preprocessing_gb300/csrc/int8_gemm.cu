@@ -58,12 +58,15 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Arrives on the even CTA's barrier at this CTA's address `bar`.
+// Arrives on the even CTA's barrier at this CTA's address `bar`.  Relaxed: what
+// it reports is that TMEM has been read, which tcgen05.wait::ld and the tcgen05
+// fence before it order; a release would wait for the thread's stores to y
+// (measured: 4000 cycles a tile).
 __device__ __forceinline__ void bar_arrive_even(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
         : "memory");
 }
 // This CTA's address `bar` in the even CTA.
@@ -147,14 +150,20 @@ __device__ __forceinline__ bool epilogue_barrier(bool flag) {
         : "memory");
     return any != 0;
 }
-// 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
+// 16 columns of this warp's 32 lanes; v holds them after tmem_wait.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
+}
+// Waits for the loads; the values pass through it, so that none is used before.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 // ---------------------------------------------------------------- copies ---
@@ -335,6 +344,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         const int quarter = warp & 3, col0 = (warp - 4) / 4 * W, me = threadIdx.x - 128;
         uint8_t* const pass = base + ST * kStageBytes<BN> + (warp - 4) * 32 * kPassBytes;
         float2* const channel = reinterpret_cast<float2*>(base + ST * kStageBytes<BN> + kEpilogueWarps * 32 * kPassBytes);
+        // a thread's row scale, and its channel's (scale, bias), loaded a tile ahead
+        struct Scales { float sx; float2 channel; };
+        auto scales_of = [&](int tile) {
+            Scales v{0.0f, make_float2(0.0f, 0.0f)};
+            if (tile >= tiles) return v;
+            const int m = tile / p.n_tiles * 256 + (int)rank * 128 + quarter * 32 + lane, n = tile % p.n_tiles * BN + me;
+            if (m < p.M) v.sx = p.x_scale[m];
+            if (me < BN && n < p.N) v.channel = make_float2(p.w_scale[n], p.bias != nullptr ? p.bias[n] : 0.0f);
+            return v;
+        };
+        Scales ahead = scales_of(pair);
         int half = 0, buf = 0;
         uint32_t half_phase = 0;
         bool ok = true;
@@ -342,14 +362,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
             // scale and bias of the tile's channels; the other buffer may still be in use
             buf ^= 1;
-            if (me < BN) {
-                const int n = nt * BN + me;
-                channel[buf * BN + me] = n < p.N ? make_float2(p.w_scale[n], p.bias != nullptr ? p.bias[n] : 0.0f)
-                                                 : make_float2(0.0f, 0.0f);
-            }
+            if (me < BN) channel[buf * BN + me] = ahead.channel;
             const int m0 = mt * 256 + (int)rank * 128 + quarter * 32;
-            const float sx = m0 + lane < p.M ? p.x_scale[m0 + lane] : 0.0f;
+            const float sx = ahead.sx;
             if (epilogue_barrier(!ok)) break;
+            ahead = scales_of(tile + pairs);
             int acc[ONE ? 1 : W];
             for (int part = 0; part < parts - 1; ++part) {
                 ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up));
@@ -361,6 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                     for (int c = 0; c < W; c += 16) {
                         uint32_t v[16];
                         tmem_load16(at + c, v);
+                        tmem_wait(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int sum = __float2int_rn(__uint_as_float(v[i]));
@@ -378,11 +396,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             tmem_fence_after();
             const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
             const int n0 = nt * BN + col0;
+            // G columns at a time; with registers to spare, the next are on their way meanwhile
+            constexpr int G = ONE ? 32 : 16;
+            uint32_t v[G], next[G];
+            auto fetch = [&](int c, uint32_t (&to)[G]) {
+                tmem_load16(at + c, to);
+                if constexpr (ONE) tmem_load16(at + c + 16, to + 16);
+            };
+            if (ONE) fetch(0, next);
 #pragma unroll
-            for (int c = 0; c < W; c += 16) {
-                uint32_t v[16];
-                tmem_load16(at + c, v);
-                if (c + 16 == W) {   // TMEM is read: the next sums may go there
+            for (int c = 0; c < W; c += G) {
+                if (!ONE) fetch(c, next);
+                tmem_wait(next);
+#pragma unroll
+                for (int i = 0; i < G; ++i) v[i] = next[i];
+                if (ONE && c + G < W) fetch(c + G, next);
+                if (c + G == W) {   // TMEM is read: the next sums may go there
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_even(sums_empty(half));
@@ -391,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 // through the warp's 2 KB, 64 bytes of each row at a time, so that rows of y are written in
                 // 64-byte runs; piece q of row r lies at q ^ (r >> 1 & 3): no bank conflicts
 #pragma unroll
-                for (int i = 0; i < 16; i += V) {
+                for (int i = 0; i < G; i += V) {
                     union { uint4 word; E e[V]; } o;
 #pragma unroll
                     for (int j = 0; j < V; j += 2) {
@@ -406,27 +435,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                     }
                     const int q = (c + i) % C / V;
                     *reinterpret_cast<uint4*>(pass + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16) = o.word;
-                }
-                if ((c + 16) % C != 0) continue;
-                __syncwarp();
-                const int n = n0 + c + 16 - C;
-                E* y = static_cast<E*>(p.y) + (long long)m0 * p.y_stride + n;
-                if (p.wide && n + C <= p.N) {
+                    if ((c + i + V) % C != 0) continue;
+                    __syncwarp();
+                    const int n = n0 + c + i + V - C;
+                    E* y = static_cast<E*>(p.y) + (long long)m0 * p.y_stride + n;
+                    if (p.wide && n + C <= p.N) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2), q = lane & 3;
-                        const uint4 o = *reinterpret_cast<const uint4*>(pass + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
-                        if (m0 + r < p.M) *reinterpret_cast<uint4*>(y + r * p.y_stride + q * V) = o;
+                        for (int d = 0; d < 4; ++d) {
+                            const int r = d * 8 + (lane >> 2), part_q = lane & 3;
+                            const uint4 w = *reinterpret_cast<const uint4*>(pass + r * 64 + ((part_q ^ (r >> 1)) & 3) * 16);
+                            if (m0 + r < p.M) *reinterpret_cast<uint4*>(y + r * p.y_stride + part_q * V) = w;
+                        }
+                    } else {
+                        constexpr int R = 32 / C;   // rows of C values at a time
+                        for (int r = lane / C; r < 32; r += R) {
+                            const int e = lane % C, part_q = e / V;
+                            const E w = *(reinterpret_cast<const E*>(pass + r * 64 + ((part_q ^ (r >> 1)) & 3) * 16) + e % V);
+                            if (m0 + r < p.M && n + e < p.N) y[r * p.y_stride + e] = w;
+                        }
                     }
-                } else {
-                    constexpr int R = 32 / C;   // rows of C values at a time
-                    for (int r = lane / C; r < 32; r += R) {
-                        const int e = lane % C, q = e / V;
-                        const E o = *(reinterpret_cast<const E*>(pass + r * 64 + ((q ^ (r >> 1)) & 3) * 16) + e % V);
-                        if (m0 + r < p.M && n + e < p.N) y[r * p.y_stride + e] = o;
-                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     }
