@@ -21,43 +21,21 @@
 #include <mutex>
 
 #include "int8_parts.h"
+#include "tensor_core.h"
 #include "token_ops.h"
 
 namespace trfn {
 namespace {
 
 __device__ unsigned int g_gemm_status;
-constexpr unsigned kStatusTimeout = 1u;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
 
 constexpr int kBlockRows = 128, kBlockK = 64, kBlockBytes = kBlockRows * kBlockK * 2;
 constexpr int kExactBlocks = 1024 / kBlockK;       // blocks of K summed in binary32
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 
-// ------------------------------------------------------------- PTX forms ---
+// ------------------------------------------------- PTX forms of the pair ---
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
 // Arrives on the even CTA's barrier at this CTA's address `bar`.  Relaxed: what
 // it reports is that TMEM has been read, which tcgen05.wait::ld and the tcgen05
 // fence before it order; a release would wait for the thread's stores to y
@@ -75,36 +53,6 @@ __device__ __forceinline__ uint32_t in_even(uint32_t bar) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
     return a;
 }
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Waits for the phase with this parity; false after about a second, or as soon
-// as another thread of the CTA gave up.
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* given_up) {
-    uint64_t t0 = 0;   // reading the timer takes longer than a product: not before the wait is a long one
-    for (uint32_t i = 1; i < (1u << 28); ++i) {
-        if (bar_try(bar, parity)) return true;
-        if ((i & 255u) == 0) {
-            if (*given_up) return false;
-            if (t0 == 0) t0 = now_ns();
-            else if (now_ns() - t0 > kWaitLimitNs) break;
-        }
-    }
-    *given_up = 1;
-    atomicOr(&g_gemm_status, kStatusTimeout);
-    return false;
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* given_up) {
-    return bar_try(bar, parity) || bar_wait_slow(bar, parity, given_up);
-}
 // Box of a tensor map at row `row`; the bytes count on `bar`, a barrier of
 // either CTA of the pair.
 __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
@@ -114,26 +62,23 @@ __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(0), "r"(row), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-// Operand rows of 128 bytes (64 binary16 along K), 128-byte swizzle, 8 rows
-// (1024 bytes) to a swizzle atom.
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Issued by the whole warp for its one elected thread: a branch around it would leave the compiler without
+// the knowledge that its operands are the warp's (measured: 85 cycles a product instead of some).
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(shape), "r"(add)
         : "memory");
 }
 // Arrives on `bar` of both CTAs when the products issued so far are done.
 __device__ __forceinline__ void commit_both(uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
 }
@@ -150,22 +95,6 @@ __device__ __forceinline__ bool epilogue_barrier(bool flag) {
         : "memory");
     return any != 0;
 }
-// 16 columns of this warp's 32 lanes; v holds them after tmem_wait.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(addr));
-}
-// Waits for the loads; the values pass through it, so that none is used before.
-template <int N>
-__device__ __forceinline__ void tmem_wait(uint32_t (&v)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
-}
-
 // ---------------------------------------------------------------- copies ---
 
 struct CopyParams {
@@ -192,7 +121,12 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
         const ByteRows m{of_w ? p.w.p : p.x.p, of_w ? p.w.stride : p.x.stride, of_w ? p.w.end : p.x.end,
                          of_w ? p.w.rows : p.x.rows, p.x.K};
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < m.rows) v = load16<ON16>(m, row, k);
+        if (row < m.rows) {
+            const int8_t* at = m.p + row * m.stride;
+            Piece<ON16> piece;
+            piece.fetch(m, at, k);
+            v = piece.value(m, at, k, false);
+        }
         uint4 a, b;
         int8_to_half(v.x, a.x, a.y);
         int8_to_half(v.y, a.z, a.w);
@@ -284,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 const int ch = nt * BN + (int)rank * (BN / 2);
                 const int wb = (ch >> 7) * p.k_blocks, sub = ch & 127;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!bar_wait(empty(s), phase ^ 1u, &given_up)) { ok = false; break; }
+                    if (!bar_wait(empty(s), phase ^ 1u, &given_up, &g_gemm_status)) { ok = false; break; }
                     const uint32_t at = ring + s * kStageBytes<BN>;
                     // both CTAs' bytes count on the even one's barrier
                     if (rank == 0) bar_expect(full(s), 2 * kStageBytes<BN>);
@@ -305,39 +239,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 }
         }
     } else if (warp == 1 && rank == 0) {
-        if (lane == 0) {
-            constexpr uint32_t shape = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);   // f16 x f16 -> f32, 256 x BN
-            int s = 0, half = 0;
-            uint32_t phase = 0, half_phase = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                for (int part = 0; part < parts && ok; ++part) {
-                    ok = bar_wait(sums_empty(half), half_phase ^ 1u, &given_up);
+        constexpr uint32_t shape = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);   // f16 x f16 -> f32, 256 x BN
+        const uint64_t x0 = operand(ring), w0 = operand(ring + kBlockBytes);
+        int s = 0, half = 0;
+        uint32_t phase = 0, half_phase = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            for (int part = 0; part < parts && ok; ++part) {
+                ok = __all_sync(0xffffffffu, bar_wait(sums_empty(half), half_phase ^ 1u, &given_up, &g_gemm_status));
+                if (!ok) break;
+                tmem_fence_after();
+                const uint32_t d = tmem + half * BN;
+                const int kb0 = part * kExactBlocks, kb1 = min(p.k_blocks, kb0 + kExactBlocks);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, &g_gemm_status));
                     if (!ok) break;
                     tmem_fence_after();
-                    const uint32_t d = tmem + half * BN;
-                    const int kb0 = part * kExactBlocks, kb1 = min(p.k_blocks, kb0 + kExactBlocks);
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        ok = bar_wait(full(s), phase, &given_up);
-                        if (!ok) break;
-                        tmem_fence_after();
-                        const uint32_t at = ring + s * kStageBytes<BN>;
+                    const uint32_t at = s * (kStageBytes<BN> / 16);   // descriptors count in 16 bytes
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 16; ++k)
-                            mma_pair(d, operand(at + 32 * k), operand(at + kBlockBytes + 32 * k), shape, kb > kb0 || k > 0);
-                        commit_both(empty(s));
-                        if (++s == ST) { s = 0; phase ^= 1u; }
-                    }
-                    commit_both(sums_full(half));
-                    if (++half == 2) { half = 0; half_phase ^= 1u; }
+                    for (int k = 0; k < kBlockK / 16; ++k)
+                        mma_pair(d, x0 + at + 2 * k, w0 + at + 2 * k, shape, kb > kb0 || k > 0);
+                    commit_both(empty(s));
+                    if (++s == ST) { s = 0; phase ^= 1u; }
                 }
+                commit_both(sums_full(half));
+                if (++half == 2) { half = 0; half_phase ^= 1u; }
             }
-            // the last products are done before TMEM is freed: their arrival on sums_full of the half before
-            const int last = half ^ 1;
-            const uint32_t last_phase = half == 0 ? half_phase ^ 1u : half_phase;
-            if (pair < tiles)
-                for (int n = 0; n < (1 << 20) && !bar_try(sums_full(last), last_phase); ++n) {}
         }
+        // the last products are done before TMEM is freed: their arrival on sums_full of the half before
+        const int last = half ^ 1;
+        const uint32_t last_phase = half == 0 ? half_phase ^ 1u : half_phase;
+        if (pair < tiles)
+            for (int n = 0; n < (1 << 20) && !bar_try(sums_full(last), last_phase); ++n) {}
+        __syncwarp();
     } else if (warp >= 4) {
         constexpr int W = BN / 2;                      // channels of a warp
         constexpr int V = 16 / sizeof(E), C = kPassBytes / sizeof(E);   // channels of 16 bytes, of a pass
@@ -369,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             ahead = scales_of(tile + pairs);
             int acc[ONE ? 1 : W];
             for (int part = 0; part < parts - 1; ++part) {
-                ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up));
+                ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, &g_gemm_status));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
@@ -391,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 if (lane == 0) bar_arrive_even(sums_empty(half));
                 if (++half == 2) { half = 0; half_phase ^= 1u; }
             }
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up));
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, &g_gemm_status));
             if (!ok) continue;   // to the barrier, where all eight warps leave together
             tmem_fence_after();
             const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
@@ -576,7 +510,7 @@ int launch_int8_gemm(const MatmulArgs& a) {
     c.xh = static_cast<uint4*>(a.workspace);
     c.wh = c.xh + c.x_pieces * 2;
     c.k_blocks = kb;
-    const bool on16 = (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.x_stride % 16 == 0 && a.w_stride % 16 == 0;
+    const bool on16 = rows_on16(a.x, a.x_stride, a.M) && rows_on16(a.w, a.w_stride, a.N);
     const long long ctas = (c.x_pieces + c.w_pieces + 255) / 256;
     const unsigned grid = (unsigned)(ctas < (1 << 30) ? ctas : (1 << 30));
     if (on16) copy_kernel<true><<<grid, 256, 0, st>>>(c);

@@ -1,27 +1,26 @@
 // y[m][n] = (sum_k x[m][k] w[n][k]) sx[m] sw[n] + bias[n] over int8 x and w:
-// the kernel for few tokens, and the choice between it and int8_gemm.cu's.
+// the kernel for up to 8 tokens, and the choice between the product's kernels.
 //
-// Arithmetic.  sm_103a has no int8 kind of tcgen05.mma, and its int8 mma.sync
-// runs at a fraction of the binary16 rate; int8 values are exact in binary16,
-// their products exact in the tensor cores, and sums of at most 1024 of them
-// (2^14 * 2^10 = 2^24) exact in binary32.  So every kernel multiplies in
-// binary16, sums 1024 products in binary32, and adds those sums as integers.
+// Arithmetic of the others (int8_mid.cu, int8_gemm.cu).  sm_103a has no int8
+// kind of tcgen05.mma, and its int8 mma.sync runs at a fraction of the
+// binary16 rate; int8 values are exact in binary16, their products exact in
+// the tensor cores, and sums of at most 1024 of them (2^14 * 2^10 = 2^24)
+// exact in binary32.  So they multiply in binary16, sum 1024 products in
+// binary32, and add those sums as integers.
 #include "int8_parts.h"
 #include "token_ops.h"
 
 namespace trfn {
 namespace {
 
-// Few tokens: bound by reading w once.  A CTA of 8 warps makes 16 R CG
-// channels x 8 J tokens: warp = (channel group of 16 R, part of K).  A warp
-// loads 64 bytes of each of its rows at a time, straight into the fragments
-// of mma.m16n8k16: a sum over k takes its terms in any order, so lane t of a
-// quad takes bytes 16 t .. 16 t + 15 of w's and x's rows alike and calls its
-// word j the fragment of the j-th of four products.  Nothing passes through
-// shared memory but the sums, which the warps add there as integers.
-constexpr int kWarps = 8;
+// Up to 8 tokens: bound by reading w once.  A warp takes kRows channels and
+// one of KP parts of K: its lanes read 512 bytes of each channel's row at a
+// time, kDepth such steps ahead, and sum four products an instruction
+// (__dp4a); the lanes' sums are added by one redux each, the parts' in shared
+// memory.  Integer sums have no order.
+constexpr int kWarps = 8, kRows = 4, kDepth = 4, kStep = 512;
 
-struct DotParams {
+struct FewParams {
     ByteRows x, w;
     const float* x_scale;
     const float* w_scale;
@@ -30,128 +29,106 @@ struct DotParams {
     long long y_stride;
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <typename E, int J, int R, int CG, int DEPTH, bool ON16>
-__global__ void __launch_bounds__(kWarps * 32) dot_kernel(const DotParams p) {
-    constexpr int NT = 16 * R * CG, MT = 8 * J, KS = kWarps / CG, S = NT + 4;   // S = 4 mod 16: no bank conflicts
-    __shared__ int sums[MT * S];
-    for (int i = threadIdx.x; i < MT * S; i += kWarps * 32) sums[i] = 0;
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int cg = warp % CG, ks = warp / CG;
-    // tiles of one channel block are neighbours: w is read from HBM once
-    const int m_tiles = (p.x.rows + MT - 1) / MT;
-    const int n0 = (int)(blockIdx.x / m_tiles) * NT, m0 = (int)(blockIdx.x % m_tiles) * MT;
-    const int wrow = n0 + cg * 16 * R + g, xrow = m0 + g;
-    const int slices = (p.x.K + 63) >> 6;
-    float acc[R][J][4];
+template <typename E, int M, int KP, bool ON16>
+__global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
+    constexpr int NT = kWarps / KP * kRows;   // channels of a CTA
+    __shared__ int sums[KP][M][NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % KP, group = warp / KP;
+    const int n0 = blockIdx.x * NT;
+    // rows past the end repeat the last: their sums are not written
+    const int8_t* wr[kRows];
+    const int8_t* xr[M];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kRows; ++r) wr[r] = p.w.p + min(n0 + group * kRows + r, p.w.rows - 1) * p.w.stride;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+    for (int m = 0; m < M; ++m) xr[m] = p.x.p + min(m, p.x.rows - 1) * p.x.stride;
+    const int steps = (p.x.K + kStep - 1) / kStep;
+    Piece<ON16> wv[kDepth][kRows];
+    auto fetch = [&](int step, Piece<ON16> (&v)[kRows]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.0f;
-
-    uint4 wv[DEPTH][2 * R], xv[DEPTH][J];
-    auto load = [&](int s, uint4 (&w)[2 * R], uint4 (&x)[J]) {
-        const int k = s * 64 + t * 16;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 2 * R; ++i)
-            w[i] = (s < slices && wrow + 8 * i < p.w.rows) ? load16<ON16>(p.w, wrow + 8 * i, k) : zero;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            x[j] = (s < slices && xrow + 8 * j < p.x.rows) ? load16<ON16>(p.x, xrow + 8 * j, k) : zero;
-    };
-    auto flush = [&]() {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int token = 8 * j + 2 * t + (i & 1), ch = (cg * R + r) * 16 + g + 8 * (i >> 1);
-                    atomicAdd(&sums[token * S + ch], __float2int_rn(acc[r][j][i]));
-                    acc[r][j][i] = 0.0f;
-                }
+        for (int r = 0; r < kRows; ++r) v[r].fetch(p.w, wr[r], step * kStep + lane * 16);
     };
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(ks + d * KS, wv[d], xv[d]);
-    int since = 0;
-    for (int s0 = ks; s0 < slices; s0 += DEPTH * KS) {
+    for (int d = 0; d < kDepth; ++d) fetch(part + d * KP, wv[d]);
+    int acc[kRows][M];
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int s = s0 + d * KS;
-            if (s < slices) {
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t a[R][4];
+        for (int m = 0; m < M; ++m) acc[r][m] = 0;
+    for (int s0 = part; s0 < steps; s0 += kDepth * KP) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        int8_to_half((&wv[d][2 * r].x)[q], a[r][0], a[r][2]);
-                        int8_to_half((&wv[d][2 * r + 1].x)[q], a[r][1], a[r][3]);
-                    }
+        for (int d = 0; d < kDepth; ++d) {
+            const int step = s0 + d * KP, k = step * kStep + lane * 16;
+            if (step < steps) {
+                Piece<ON16> xv[M];
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        uint32_t b0, b1;
-                        int8_to_half((&xv[d][j].x)[q], b0, b1);
+                for (int m = 0; m < M; ++m) xv[m].fetch(p.x, xr[m], k);
+                uint4 w[kRows];
 #pragma unroll
-                        for (int r = 0; r < R; ++r) mma_16816(acc[r][j], a[r][0], a[r][1], a[r][2], a[r][3], b0, b1);
+                for (int r = 0; r < kRows; ++r) w[r] = wv[d][r].value(p.w, wr[r], k, false);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const uint4 x = xv[m].value(p.x, xr[m], k, false);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        acc[r][m] = __dp4a((int)w[r].x, (int)x.x, acc[r][m]);
+                        acc[r][m] = __dp4a((int)w[r].y, (int)x.y, acc[r][m]);
+                        acc[r][m] = __dp4a((int)w[r].z, (int)x.z, acc[r][m]);
+                        acc[r][m] = __dp4a((int)w[r].w, (int)x.w, acc[r][m]);
                     }
                 }
-                load(s + DEPTH * KS, wv[d], xv[d]);
-                if (++since == 16) {   // 1024 products: the last exact binary32 sum
-                    flush();
-                    since = 0;
-                }
+                fetch(step + kDepth * KP, wv[d]);
             }
         }
     }
-    if (since > 0) flush();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
+            if (lane == 0) sums[part][m][group * kRows + r] = sum;
+        }
     __syncthreads();
-    E* y = static_cast<E*>(p.y);
-    for (int i = threadIdx.x; i < MT * NT; i += kWarps * 32) {
-        const int token = i / NT, ch = i % NT;
-        const int m = m0 + token, n = n0 + ch;
+    if (threadIdx.x < M * NT) {
+        const int m = threadIdx.x / NT, c = threadIdx.x % NT, n = n0 + c;
         if (m < p.x.rows && n < p.w.rows) {
-            float v = (float)sums[token * S + ch] * p.x_scale[m] * p.w_scale[n];
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < KP; ++i) sum += sums[i][m][c];
+            float v = (float)sum * p.x_scale[m] * p.w_scale[n];
             if (p.bias != nullptr) v += p.bias[n];
-            y[m * p.y_stride + n] = out_value<E>(v);
+            static_cast<E*>(p.y)[m * p.y_stride + n] = out_value<E>(v);
         }
     }
 }
 
-template <typename E, int J, int R, int CG, int DEPTH>
-void start_dot(const DotParams& p, bool on16, cudaStream_t st) {
-    const unsigned grid = (unsigned)((p.w.rows + 16 * R * CG - 1) / (16 * R * CG)) * ((p.x.rows + 8 * J - 1) / (8 * J));
-    if (on16) dot_kernel<E, J, R, CG, DEPTH, true><<<grid, kWarps * 32, 0, st>>>(p);
-    else dot_kernel<E, J, R, CG, DEPTH, false><<<grid, kWarps * 32, 0, st>>>(p);
+template <typename E, int M, int KP>
+void start_few(const FewParams& p, bool on16, cudaStream_t st) {
+    constexpr int NT = kWarps / KP * kRows;
+    const unsigned grid = (unsigned)((p.w.rows + NT - 1) / NT);
+    if (on16) few_kernel<E, M, KP, true><<<grid, kWarps * 32, 0, st>>>(p);
+    else few_kernel<E, M, KP, false><<<grid, kWarps * 32, 0, st>>>(p);
+}
+
+template <typename E, int M>
+void part_few(const FewParams& p, bool on16, cudaStream_t st) {
+    // K in parts where the channels alone do not give each SM two CTAs
+    if (p.w.rows >= 304 * kWarps * kRows) start_few<E, M, 1>(p, on16, st);
+    else if (p.w.rows >= 304 * kWarps * kRows / 4) start_few<E, M, 2>(p, on16, st);
+    else start_few<E, M, 8>(p, on16, st);
 }
 
 template <typename E>
-void pick_dot(const DotParams& p, bool on16, cudaStream_t st) {
-    const int M = p.x.rows;
-    if (M <= 8) start_dot<E, 1, 1, 1, 4>(p, on16, st);
-    else if (M <= 16) start_dot<E, 2, 1, 1, 4>(p, on16, st);
-    else if (M <= 32) start_dot<E, 4, 1, 1, 2>(p, on16, st);
-    else start_dot<E, 8, 2, 4, 1>(p, on16, st);
+void pick_few(const FewParams& p, bool on16, cudaStream_t st) {
+    if (p.x.rows == 1) part_few<E, 1>(p, on16, st);
+    else if (p.x.rows == 2) part_few<E, 2>(p, on16, st);
+    else if (p.x.rows <= 4) part_few<E, 4>(p, on16, st);
+    else part_few<E, 8>(p, on16, st);
 }
 
-}  // namespace
-
-bool dot_takes(long long M, long long N, long long K) {
-    return M <= 64 || (double)M * (double)N * (double)K <= (double)(1 << 30);
-}
-
-int launch_int8_dot(const MatmulArgs& a) {
-    DotParams p;
+int launch_few(const MatmulArgs& a) {
+    FewParams p;
     p.x = ByteRows{a.x, a.x_stride, a.x + (a.M - 1) * a.x_stride + a.K, a.M, a.K};
     p.w = ByteRows{a.w, a.w_stride, a.w + (a.N - 1) * a.w_stride + a.K, a.N, a.K};
     p.x_scale = a.x_scale;
@@ -159,21 +136,27 @@ int launch_int8_dot(const MatmulArgs& a) {
     p.bias = a.bias;
     p.y = a.y;
     p.y_stride = a.y_stride;
-    const bool on16 = (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.w % 16 == 0 && (a.M <= 1 || a.x_stride % 16 == 0) &&
-                      (a.N <= 1 || a.w_stride % 16 == 0);
+    const bool on16 = rows_on16(a.x, a.x_stride, a.M) && rows_on16(a.w, a.w_stride, a.N);
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-    if (a.out_dtype == TR_ELEM_F32) pick_dot<float>(p, on16, st);
-    else if (a.out_dtype == TR_ELEM_F16) pick_dot<__half>(p, on16, st);
-    else pick_dot<__nv_bfloat16>(p, on16, st);
-    return launched("int8 dot kernel");
+    if (a.out_dtype == TR_ELEM_F32) pick_few<float>(p, on16, st);
+    else if (a.out_dtype == TR_ELEM_F16) pick_few<__half>(p, on16, st);
+    else pick_few<__nv_bfloat16>(p, on16, st);
+    return launched("int8 product kernel (few tokens)");
 }
 
+bool mid_takes(long long M, long long N, long long K) {
+    return M <= 256 || (double)M * (double)N * (double)K <= 4e9;
+}
+
+}  // namespace
+
 size_t int8_matmul_workspace(long long M, long long N, long long K) {
-    return dot_takes(M, N, K) ? 0 : int8_gemm_workspace(M, N, K);
+    return M <= 2 || mid_takes(M, N, K) ? 0 : int8_gemm_workspace(M, N, K);
 }
 
 int launch_int8_matmul(const MatmulArgs& a) {
-    return dot_takes(a.M, a.N, a.K) ? launch_int8_dot(a) : launch_int8_gemm(a);
+    if (a.M <= 2) return launch_few(a);
+    return mid_takes(a.M, a.N, a.K) ? launch_int8_mid(a) : launch_int8_gemm(a);
 }
 
 }  // namespace trfn

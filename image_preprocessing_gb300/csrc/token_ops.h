@@ -75,8 +75,11 @@ size_t int8_matmul_workspace(long long M, long long N, long long K);
 // many tokens (int8_gemm.cu): binary16 copies in the workspace, tcgen05
 int launch_int8_gemm(const MatmulArgs& a);
 size_t int8_gemm_workspace(long long M, long long N, long long K);
-// Status bits its kernel left on the current device (as read_device_status).
+// tokens in between (int8_mid.cu): tcgen05 on tiles converted on the way
+int launch_int8_mid(const MatmulArgs& a);
+// Status bits their kernels left on the current device (as read_device_status).
 int read_gemm_status(int* flags, bool clear);
+int read_mid_status(int* flags, bool clear);
 
 // cudaGetLastError() after a launch as a tr_status; counts the launch.
 int launched(const char* what);
