@@ -18,6 +18,7 @@
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <mutex>
 
 #include "int8_parts.h"
@@ -483,11 +484,15 @@ int pick_parts(const GemmParams& p, const Copies& c, cudaStream_t st) {
     return p.k_blocks <= kExactBlocks ? start_gemm<E, BN, true>(p, c, st) : start_gemm<E, BN, false>(p, c, st);
 }
 
+// Cycles of the product with tiles of BN channels, for a block of K: one wave of pairs takes 512 cycles of the
+// tensor cores (BN = 256) or, bound by loading, 340 (BN = 128; 256 by the tensor cores).
+double wave_cycles(long long M, long long N, int BN) {
+    return std::ceil(std::ceil(M / 256.0) * std::ceil((double)N / BN) / 76) * (BN == 256 ? 512 : 340);
+}
+
 template <typename E>
 int pick_gemm(const GemmParams& p, const Copies& c, cudaStream_t st) {
-    // the narrower tile where the wide one leaves pairs of SMs without any
-    const long long wide = (long long)pieces_of(p.M, 256) * pieces_of(p.N, 256);
-    return wide >= 76 ? pick_parts<E, 256>(p, c, st) : pick_parts<E, 128>(p, c, st);
+    return wave_cycles(p.M, p.N, 256) <= wave_cycles(p.M, p.N, 128) ? pick_parts<E, 256>(p, c, st) : pick_parts<E, 128>(p, c, st);
 }
 
 }  // namespace
@@ -496,6 +501,12 @@ size_t int8_gemm_workspace(long long M, long long N, long long K) {
     const size_t kb = (size_t)((K + kBlockK - 1) / kBlockK);
     // whole tiles of 256 rows: the product reads them without looking at M and N
     return (size_t)((M + 255) / 256 + (N + 255) / 256) * 2 * kb * kBlockBytes;
+}
+
+// Start of two kernels, the copies' bytes (read one, write two) at 2850 a cycle, and the product.
+double int8_gemm_cycles(long long M, long long N, long long K) {
+    return 9500 + 3.0 * (double)(M + N) * (double)K / 2850 +
+           std::ceil((double)K / kBlockK) * std::fmin(wave_cycles(M, N, 256), wave_cycles(M, N, 128));
 }
 
 int launch_int8_gemm(const MatmulArgs& a) {

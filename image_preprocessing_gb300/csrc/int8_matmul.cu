@@ -1,5 +1,5 @@
 // y[m][n] = (sum_k x[m][k] w[n][k]) sx[m] sw[n] + bias[n] over int8 x and w:
-// the kernel for up to 8 tokens, and the choice between the product's kernels.
+// the kernel for one or two tokens, and the choice between the product's kernels.
 //
 // Arithmetic of the others (int8_mid.cu, int8_gemm.cu).  sm_103a has no int8
 // kind of tcgen05.mma, and its int8 mma.sync runs at a fraction of the
@@ -13,12 +13,12 @@
 namespace trfn {
 namespace {
 
-// Up to 8 tokens: bound by reading w once.  A warp takes kRows channels and
+// One or two tokens: bound by reading w once.  A warp takes kRows channels and
 // one of KP parts of K: its lanes read 512 bytes of each channel's row at a
 // time, kDepth such steps ahead, and sum four products an instruction
 // (__dp4a); the lanes' sums are added by one redux each, the parts' in shared
 // memory.  Integer sums have no order.
-constexpr int kWarps = 8, kRows = 4, kDepth = 4, kStep = 512;
+constexpr int kWarps = 8, kRows = 4, kDepth = 2, kStep = 512;
 
 struct FewParams {
     ByteRows x, w;
@@ -113,18 +113,16 @@ void start_few(const FewParams& p, bool on16, cudaStream_t st) {
 
 template <typename E, int M>
 void part_few(const FewParams& p, bool on16, cudaStream_t st) {
-    // K in parts where the channels alone do not give each SM two CTAs
-    if (p.w.rows >= 304 * kWarps * kRows) start_few<E, M, 1>(p, on16, st);
-    else if (p.w.rows >= 304 * kWarps * kRows / 4) start_few<E, M, 2>(p, on16, st);
+    // K in 8 parts where the channels alone do not give each SM four CTAs of two
+    // (1 x 4096 x 16384: 15.1 us in 2 parts, 14.8 in 8; 1 x 16384 x 4096: 14.9 and 17.7)
+    if (p.w.rows >= 152 * kWarps * kRows / 2) start_few<E, M, 2>(p, on16, st);
     else start_few<E, M, 8>(p, on16, st);
 }
 
 template <typename E>
 void pick_few(const FewParams& p, bool on16, cudaStream_t st) {
     if (p.x.rows == 1) part_few<E, 1>(p, on16, st);
-    else if (p.x.rows == 2) part_few<E, 2>(p, on16, st);
-    else if (p.x.rows <= 4) part_few<E, 4>(p, on16, st);
-    else part_few<E, 8>(p, on16, st);
+    else part_few<E, 2>(p, on16, st);
 }
 
 int launch_few(const MatmulArgs& a) {
@@ -144,9 +142,8 @@ int launch_few(const MatmulArgs& a) {
     return launched("int8 product kernel (few tokens)");
 }
 
-bool mid_takes(long long M, long long N, long long K) {
-    return M <= 256 || (double)M * (double)N * (double)K <= 4e9;
-}
+// By shape alone, so that the workspace is known before the matrices are.
+bool mid_takes(long long M, long long N, long long K) { return int8_mid_cycles(M, N, K) <= int8_gemm_cycles(M, N, K); }
 
 }  // namespace
 

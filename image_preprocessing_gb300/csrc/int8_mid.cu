@@ -4,17 +4,20 @@
 // Bound by reading w once while tokens are few, by converting it after.  The
 // weights are the product's 128 rows, so that a tile of 16 to 128 tokens fills
 // it whatever their number: a CTA, one to an SM, makes 128 channels x T tokens
-// over a part of K, in blocks of 64 values.  Four groups of four warps take
-// every fourth block: they copy its int8 into shared memory, 100 KB ahead (what
-// one SM must have under way to get its share of the HBM rate), and write what
-// has landed as binary16 into their swizzled stage; a thread copies and
-// converts the same bytes, so the copies need no barrier.  One more thread
-// issues tcgen05 products of 128 x T x 16 into TMEM.  Where the tiles are fewer
-// than the SMs, a cluster of up to 8 CTAs shares a tile, a part of K each, and
-// adds its sums through distributed shared memory as integers, which have no
-// order.
+// over a part of K, in blocks of 64 values.  Three or four groups of four warps
+// take the blocks in turn: they copy int8 into shared memory, 70 KB ahead and
+// more (what one SM must have under way to get its share of the HBM rate), and
+// write what has landed as binary16 into swizzled stages, of which each group
+// has two, so that it converts while its last block is multiplied; a thread copies and
+// converts the same bytes, so the copies need no barrier.  Each group has a
+// thread more that issues its tcgen05 products of 128 x T x 16 (one thread for
+// all takes 500 cycles a block, the HBM rate allows 300), into sums of its own
+// in TMEM.  Where the tiles are fewer than the SMs, a cluster of up to 8 CTAs
+// shares a tile, a part of K each, and adds its sums through distributed shared
+// memory.  All of these are added as integers, which have no order.
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "int8_parts.h"
@@ -27,8 +30,14 @@ namespace {
 __device__ unsigned int g_mid_status;
 
 constexpr int kRows = 128, kBlockK = 64, kExactBlocks = 1024 / kBlockK;
-constexpr int kGroups = 4, kGroup = 128;                                  // groups of converting threads
-constexpr int kConvert = kGroups * kGroup, kThreads = kConvert + 32;      // and a warp that issues
+constexpr int kGroup = 128;                                    // threads of a group
+template <int T> constexpr int kGroups = T == 16 || T == 128 ? 4 : 3;
+template <int T> constexpr int kConvert = kGroups<T> * kGroup;
+// warps that issue products, each into T columns of TMEM, and all threads
+template <int T> constexpr int kIssuers = T == 128 ? 2 : kGroups<T>;
+template <int T> constexpr int kThreads = kConvert<T> + 32 * kIssuers<T>;
+// blocks to a sum of 1024 products in every issuer's columns
+template <int T> constexpr int kPartBlocks = kExactBlocks * kIssuers<T>;
 
 struct MidParams {
     ByteRows x, w;
@@ -45,8 +54,10 @@ struct MidParams {
 // the threads' order.
 template <int T> constexpr int kStageBytes = (kRows + T) * 128;
 template <int T> constexpr int kRingBytes = (kRows + T) * kBlockK;
-template <int T> constexpr int kDeep = T == 16 ? 4 : T == 32 ? 3 : T == 64 ? 2 : 1;   // blocks of the ring for a group
-template <int T> constexpr int kSmemBytes = 1024 + kGroups * (kStageBytes<T> + kDeep<T> * kRingBytes<T>);
+template <int T> constexpr int kSlots = T == 128 ? 1 : 2;                  // stages of a group
+template <int T> constexpr int kStages = kGroups<T> * kSlots<T>;
+template <int T> constexpr int kDeep = T == 32 ? 3 : T == 128 ? 1 : 2;     // blocks of the ring for a group
+template <int T> constexpr int kSmemBytes = 1024 + kStages<T> * kStageBytes<T> + kGroups<T> * kDeep<T> * kRingBytes<T>;
 constexpr int kPass = kGroup / 4;                                                     // rows of a group's threads
 template <int T> constexpr int kPieces = T < kPass ? 1 : T / kPass;                   // of x, for a thread and block
 
@@ -90,30 +101,32 @@ __device__ __forceinline__ void copy16(uint32_t dst, const int8_t* src, int byte
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// ONE: at most 1024 products to a sum of this CTA.  ON16: rows on 16-byte
+// ONE: at most 1024 products to each sum in TMEM.  ON16: rows on 16-byte
 // boundaries; others pass through registers, two blocks ahead.
 template <typename E, int T, bool ONE, bool ON16>
-__global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
-    constexpr int WP = kRows / kPass, XP = kPieces<T>, DEEP = kDeep<T>, COLS = T < 32 ? 32 : T;
+__global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) {
+    constexpr int WP = kRows / kPass, XP = kPieces<T>, DEEP = kDeep<T>, NI = kIssuers<T>, PART = kPartBlocks<T>;
+    constexpr int GR = kGroups<T>, SL = kSlots<T>, ST = kStages<T>, CONVERT = kConvert<T>, COLS = T == 16 || NI == 2 ? NI * T : 4 * T;
     extern __shared__ uint8_t smem_raw[];
-    // full[4] empty[4] sums freed
-    __shared__ __align__(8) uint64_t bars[2 * kGroups + 2];
+    // full[ST] empty[ST] sums freed
+    __shared__ __align__(8) uint64_t bars[2 * ST + 2];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int given_up;
     __shared__ float x_scale[T];
+    __shared__ float2 channel[kRows];   // scale and bias
     uint8_t* const stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* const ring = stages + kGroups * kStageBytes<T>;
+    uint8_t* const ring = stages + ST * kStageBytes<T>;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (kGroups + s); };
-    const uint32_t sums = bar0 + 8u * (2 * kGroups), freed = bar0 + 8u * (2 * kGroups + 1);
+    auto empty = [&](int s) { return bar0 + 8u * (ST + s); };
+    const uint32_t sums = bar0 + 8u * (2 * ST), freed = bar0 + 8u * (2 * ST + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
     const int tile = blockIdx.x / p.split;
     const int m0 = tile % p.m_tiles * p.tokens, n0 = tile / p.m_tiles * kRows;
     const int kb0 = rank * p.blocks;
     const int nkb = max(0, min((p.x.K + kBlockK - 1) / kBlockK - kb0, p.blocks));
-    const int parts = (nkb + kExactBlocks - 1) / kExactBlocks;
+    const int parts = (nkb + PART - 1) / PART;
 
     // a thread's pieces of a block: 16 bytes of every 32nd row of w and of x.  A warp takes 64 bytes of 8 rows:
     // neither loads nor stores conflict
@@ -122,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
     const int8_t* xr[XP];
     Piece<false> wv[WP], xv[XP];   // unused with ON16
     auto x_mine = [&](int j) { return row0 + kPass * j < p.tokens; };
-    // block i is the group's (i / 4)th
-    auto slot = [&](int i) { return (group * DEEP + i / kGroups % DEEP) * kRingBytes<T> + me * 16; };
+    // block i is the group's (i / GR)th, in its stage i / GR % SL
+    auto slot = [&](int i) { return (group * DEEP + i / GR % DEEP) * kRingBytes<T> + me * 16; };
     auto fetch = [&](int i) {
         const int k = (kb0 + i) * kBlockK + q * 16;
         if constexpr (ON16) {
@@ -146,24 +159,23 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
             for (int j = 0; j < XP; ++j) xv[j].fetch(p.x, xr[j], x_mine(j) ? kk : p.x.K);
         }
     };
-    if (tid < kConvert) {
+    if (tid < CONVERT) {
         // rows past the end repeat the last: their sums are not written
 #pragma unroll
         for (int j = 0; j < WP; ++j) wr[j] = p.w.p + (long long)min(n0 + row0 + kPass * j, p.w.rows - 1) * p.w.stride;
 #pragma unroll
         for (int j = 0; j < XP; ++j) xr[j] = p.x.p + (long long)min(m0 + row0 + kPass * j, p.x.rows - 1) * p.x.stride;
 #pragma unroll 1
-        for (int d = 0; d < (ON16 ? DEEP : 1); ++d) fetch(group + kGroups * d);
-        if (tid < p.tokens) x_scale[tid] = m0 + tid < p.x.rows ? p.x_scale[m0 + tid] : 0.0f;
-    } else {
+        for (int d = 0; d < (ON16 ? DEEP : 1); ++d) fetch(group + GR * d);
+    } else if (warp == CONVERT / 32) {
         if (lane == 0) {
             given_up = 0;
-            for (int s = 0; s < kGroups; ++s) {
+            for (int s = 0; s < ST; ++s) {
                 bar_init(full(s), kGroup / 32);
                 bar_init(empty(s), 1);
             }
-            bar_init(sums, 1);
-            bar_init(freed, kConvert / 32);
+            bar_init(sums, NI);
+            bar_init(freed, CONVERT / 32);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
@@ -178,25 +190,33 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
     const uint32_t tmem = tmem_at;
     bool ok = true;
 
-    if (warp == kConvert / 32) {
+    if (warp >= CONVERT / 32) {
+        const int issuer = warp - CONVERT / 32;   // takes blocks issuer, issuer + NI, ...
         const uint32_t shape = (1u << 4) | ((uint32_t)(p.tokens / 8) << 17) | (8u << 24);   // f16 x f16 -> f32, 128 x tokens
         const uint64_t w0 = operand(smem_u32(stages)), x0 = operand(smem_u32(stages) + kRows * 128);
-        int s = 0;
+        const uint32_t d = tmem + issuer * T;
+        int s = issuer * SL, slot_of = 0;   // stages in the order of the blocks: slot 0 of each group, slot 1 ...
         uint32_t phase = 0;
         for (int part = 0; part < parts && ok; ++part) {
             if (part > 0) ok = __all_sync(0xffffffffu, bar_wait(freed, (part - 1) & 1, &given_up, &g_mid_status));
             if (!ok) break;
             tmem_fence_after();
-            const int i0 = part * kExactBlocks, i1 = min(nkb, i0 + kExactBlocks);
-            for (int i = i0; i < i1; ++i) {
+            const int i0 = part * PART + issuer, i1 = min(nkb, (part + 1) * PART);
+            for (int i = i0; i < i1; i += NI) {
                 ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, &g_mid_status));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t at = s * (kStageBytes<T> / 16);   // descriptors count in 16 bytes
 #pragma unroll
-                for (int k = 0; k < kBlockK / 16; ++k) mma_one(tmem, w0 + at + 2 * k, x0 + at + 2 * k, shape, i > i0 || k > 0);
+                for (int k = 0; k < kBlockK / 16; ++k) mma_one(d, w0 + at + 2 * k, x0 + at + 2 * k, shape, i > i0 || k > 0);
                 commit(empty(s));
-                if (++s == kGroups) { s = 0; phase ^= 1u; }
+                if constexpr (NI == GR) {        // one group's stages in turn
+                    if (++slot_of == SL) { slot_of = 0; phase ^= 1u; }
+                    s = issuer * SL + slot_of;
+                } else {                         // every second group's one stage
+                    s += NI;
+                    if (s >= ST) { s = issuer; phase ^= 1u; }
+                }
             }
             commit(sums);
             // after a wait that ran out: what was issued is done before TMEM is freed
@@ -206,19 +226,43 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
         __syncwarp();
     }
 
-    constexpr int QT = T / 4, G = QT < 16 ? QT : 16;   // tokens of a warp, columns read at a time
-    const int quarter = warp & 3, c_warp = (warp >> 2) * QT, ch = quarter * 32 + lane;
-    const uint32_t tmem_mine = tmem + c_warp + ((uint32_t)(quarter * 32) << 16);
-    int acc[ONE ? 1 : QT];
-    if (tid < kConvert) {
-        uint32_t phase = 1;   // of the group's stage, free at first
-        uint8_t* const stage = stages + group * kStageBytes<T>;
-        for (int i = group; i < nkb; i += kGroups) {
+    // a warp reads a quarter of the channels, and every GR-th G tokens
+    constexpr int G = T / 4 < 16 ? T / 4 : 16, U = (T / G + GR - 1) / GR;
+    const int quarter = warp & 3, ch = quarter * 32 + lane;
+    const uint32_t tmem_mine = tmem + ((uint32_t)(quarter * 32) << 16);
+    auto column = [&](int u) { return ((warp >> 2) + GR * u) * G; };
+    // the sum of the issuers' sums of one part at columns c .. c+G-1; an issuer without blocks
+    // in the part has written none
+    auto read_sums = [&](int c, int blocks, int (&v)[G]) {
+        uint32_t f[NI][G];
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            if (j < blocks) tmem_load(tmem_mine + j * T + c, f[j]);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) tmem_wait(f[j]);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            v[i] = 0;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                if (j < blocks) v[i] += __float2int_rn(__uint_as_float(f[j][i]));
+        }
+    };
+    int acc[ONE ? 1 : U][G];
+    if (tid < CONVERT) {
+        // scales are on their way while the sums are made
+        const float my_scale = tid < p.tokens && m0 + tid < p.x.rows ? p.x_scale[m0 + tid] : 0.0f;
+        float2 my_channel = make_float2(0.0f, 0.0f);
+        if (tid < kRows && n0 + tid < p.w.rows)
+            my_channel = make_float2(p.w_scale[n0 + tid], p.bias != nullptr ? p.bias[n0 + tid] : 0.0f);
+        int at = group * SL;
+        uint32_t phase = 1;   // of the group's stages, free at first
+        for (int i = group; i < nkb; i += GR) {
             const int k = (kb0 + i) * kBlockK + q * 16;
             if constexpr (ON16) asm volatile("cp.async.wait_group %0;" ::"n"(DEEP - 1) : "memory");
-            ok = __all_sync(0xffffffffu, bar_wait(empty(group), phase, &given_up, &g_mid_status));
+            ok = __all_sync(0xffffffffu, bar_wait(empty(at), phase, &given_up, &g_mid_status));
             if (!ok) break;
-            phase ^= 1u;
+            uint8_t* const stage = stages + at * kStageBytes<T>;
             auto put = [&](uint8_t* rows, int r, const uint4& v) {
                 uint4 a, b;
                 int8_to_half(v.x, a.x, a.y);
@@ -242,25 +286,23 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
                              : xv[j].value(p.x, xr[j], k, false));
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the tensor cores read it next
             __syncwarp();
-            if (lane == 0) bar_arrive(full(group));
-            fetch(i + kGroups * (ON16 ? DEEP : 1));
+            if (lane == 0) bar_arrive(full(at));
+            if (++at == (group + 1) * SL) { at = group * SL; phase ^= 1u; }
+            fetch(i + GR * (ON16 ? DEEP : 1));
             if constexpr (!ONE) {
-                const int done = i / kExactBlocks + 1;   // parts converted when this was the group's last block of one
-                if (i % kExactBlocks >= kExactBlocks - kGroups && done * kExactBlocks < nkb) {
-                    // a sum of 1024 products, and more to come
+                const int done = i / PART + 1;   // parts converted, when this was the group's last block of one
+                if (i % PART >= PART - GR && done * PART < nkb) {
+                    // sums of 1024 products, and more to come
                     ok = __all_sync(0xffffffffu, bar_wait(sums, (done - 1) & 1, &given_up, &g_mid_status));
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
-                    for (int c = 0; c < QT; c += G) {
-                        uint32_t v[G];
-                        tmem_load(tmem_mine + c, v);
-                        tmem_wait(v);
+                    for (int u = 0; u < U; ++u) {
+                        if (column(u) >= p.tokens) continue;
+                        int v[G];
+                        read_sums(column(u), PART, v);
 #pragma unroll
-                        for (int j = 0; j < G; ++j) {
-                            const int sum = __float2int_rn(__uint_as_float(v[j]));
-                            acc[c + j] = done == 1 ? sum : acc[c + j] + sum;
-                        }
+                        for (int j = 0; j < G; ++j) acc[u][j] = done == 1 ? v[j] : acc[u][j] + v[j];
                     }
                     tmem_fence_before();
                     __syncwarp();
@@ -271,32 +313,28 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
         if constexpr (ON16) asm volatile("cp.async.wait_all;" ::: "memory");
         if (ok && parts > 0) ok = bar_wait(sums, (parts - 1) & 1, &given_up, &g_mid_status);
         ok = __all_sync(0xffffffffu, ok);
-        // the sums of several CTAs go over stages and ring: every thread is done with its part of them
-        if (p.split > 1) asm volatile("bar.sync 1, 512;" ::: "memory");
+        if (tid < p.tokens) x_scale[tid] = my_scale;
+        if (tid < kRows) channel[tid] = my_channel;
+        // every thread is done with its part of the stages and the ring, where a cluster's sums go
+        asm volatile("bar.sync 1, %0;" ::"n"(CONVERT) : "memory");
         if (ok) {
             tmem_fence_after();
             const int n = n0 + ch;
-            float sw = 0.0f, bias = 0.0f;
-            if (p.split == 1 && n < p.w.rows) {
-                sw = p.w_scale[n];
-                if (p.bias != nullptr) bias = p.bias[n];
-            }
+            const float sw = channel[ch].x, bias = channel[ch].y;
             E* y = static_cast<E*>(p.y) + m0 * p.y_stride + n;
             int* const dump = reinterpret_cast<int*>(stages);
 #pragma unroll
-            for (int c = 0; c < QT; c += G) {
-                if (c_warp + c >= p.tokens) break;
-                uint32_t v[G];
-                if (parts > 0) {
-                    tmem_load(tmem_mine + c, v);
-                    tmem_wait(v);
-                }
+            for (int u = 0; u < U; ++u) {
+                const int c = column(u);
+                if (c >= p.tokens) continue;
+                int v[G];
+                read_sums(c, nkb - max(parts - 1, 0) * PART, v);
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const int token = c_warp + c + j;
-                    int sum = parts > 0 ? __float2int_rn(__uint_as_float(v[j])) : 0;
+                    const int token = c + j;
+                    int sum = v[j];
                     if constexpr (!ONE)
-                        if (parts > 1) sum += acc[c + j];
+                        if (parts > 1) sum += acc[u][j];
                     if (p.split > 1) dump[token * kRows + ch] = sum;
                     else if (n < p.w.rows && m0 + token < p.x.rows)
                         y[token * p.y_stride] = out_value<E>((float)sum * x_scale[token] * sw + bias);
@@ -308,15 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
     if (p.split > 1) {
         __syncwarp();
         cluster_sync();   // every CTA's sums are in its shared memory
-        if (tid < kConvert) {
+        if (tid < CONVERT) {
             const int c4 = (tid & 31) * 4, n = n0 + c4;
             float sw[4], bias[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sw[j] = n + j < p.w.rows ? p.w_scale[n + j] : 0.0f;
-                bias[j] = n + j < p.w.rows && p.bias != nullptr ? p.bias[n + j] : 0.0f;
-            }
-            for (int i = warp; rank + p.split * i < p.tokens; i += kConvert / 32) {
+            for (int j = 0; j < 4; ++j) { sw[j] = channel[c4 + j].x; bias[j] = channel[c4 + j].y; }
+            for (int i = warp; rank + p.split * i < p.tokens; i += CONVERT / 32) {
                 const int token = rank + p.split * i, m = m0 + token;
                 if (m >= p.x.rows) break;
                 const uint32_t at = smem_u32(stages) + (token * kRows + c4) * 4;
@@ -350,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) mid_kernel(const MidParams p) {
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     }
     __syncthreads();
-    if (warp == kConvert / 32) {
+    if (warp == CONVERT / 32) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(COLS) : "memory");
     }
@@ -372,7 +407,7 @@ int start_mid(const MidParams& p, cudaStream_t st) {
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(pieces_of(p.w.rows, kRows) * p.m_tiles * p.split));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<T>);
     cfg.dynamicSmemBytes = kSmemBytes<T>;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -391,7 +426,7 @@ int start_mid(const MidParams& p, cudaStream_t st) {
 
 template <typename E, int T>
 int pick_mid(const MidParams& p, bool on16, cudaStream_t st) {
-    if (p.blocks <= kExactBlocks) return on16 ? start_mid<E, T, true, true>(p, st) : start_mid<E, T, true, false>(p, st);
+    if (p.blocks <= kPartBlocks<T>) return on16 ? start_mid<E, T, true, true>(p, st) : start_mid<E, T, true, false>(p, st);
     return on16 ? start_mid<E, T, false, true>(p, st) : start_mid<E, T, false, false>(p, st);
 }
 
@@ -405,18 +440,21 @@ int tile_mid(const MidParams& p, int T, bool on16, cudaStream_t st) {
     }
 }
 
-// Tile and split by an estimate in cycles: a start, a cost for each block, and for adding a cluster's sums.
-struct MidPlan { int T, split; long long cycles; };
+// Tile and split by an estimate in cycles, fitted to measurements from 9 x 300 x 300 to 4096 x 16384 x 4096:
+// a start, a cost for each block of K, and for adding a cluster's sums.
+struct MidPlan { int T, split; double cycles; };
 MidPlan plan_mid(long long M, long long N, long long K) {
-    MidPlan best{0, 1, 0};
-    const int tiles[4] = {16, 32, 64, 128}, cost[4] = {300, 310, 330, 450};
-    const int splits[4] = {1, 2, 4, 8}, room[4] = {152, 152, 144, 120};   // CTAs that run at once in such clusters
+    MidPlan best{0, 1, 0.0};
+    constexpr int tiles[4] = {16, 32, 64, 128}, cost[4] = {380, 430, 520, 1000};
+    constexpr int splits[4] = {1, 2, 4, 8}, room[4] = {152, 152, 144, 120};   // CTAs that run at once in such clusters
+    const double blocks = std::ceil((double)K / kBlockK), n_tiles = std::ceil((double)N / kRows);
+    const double slow = K % 16 == 0 ? 1.0 : 2.0;   // contiguous rows off 16-byte boundaries
     for (int i = 0; i < 4; ++i) {
-        const long long at = pieces_of(M, tiles[i]) * pieces_of(N, kRows), blocks = pieces_of(K, kBlockK);
+        const double at = std::ceil((double)M / tiles[i]) * n_tiles;
         for (int j = 0; j < 4 && (j == 0 || blocks >= 4 * splits[j]); ++j) {
-            const long long waves = pieces_of(at * splits[j], room[j]);
-            const long long c = waves * (5000 + pieces_of(blocks, splits[j]) * cost[i] + (j > 0 ? 2000 + 30 * tiles[i] : 0) +
-                                         tiles[i] * 8);
+            const double c = std::ceil(at * splits[j] / room[j]) *
+                             (5000 + std::ceil(blocks / splits[j]) * cost[i] * slow + (j > 0 ? 2000 + 30 * tiles[i] : 0) +
+                              tiles[i] * 8);
             if (best.T == 0 || c < best.cycles) best = MidPlan{tiles[i], splits[j], c};
         }
     }
@@ -448,6 +486,8 @@ int launch_int8_mid(const MatmulArgs& a) {
     if (a.out_dtype == TR_ELEM_F16) return tile_mid<__half>(p, plan.T, on16, st);
     return tile_mid<__nv_bfloat16>(p, plan.T, on16, st);
 }
+
+double int8_mid_cycles(long long M, long long N, long long K) { return plan_mid(M, N, K).cycles; }
 
 int read_mid_status(int* flags, bool clear) {
     unsigned v = 0;

@@ -77,6 +77,9 @@ int launch_int8_gemm(const MatmulArgs& a);
 size_t int8_gemm_workspace(long long M, long long N, long long K);
 // tokens in between (int8_mid.cu): tcgen05 on tiles converted on the way
 int launch_int8_mid(const MatmulArgs& a);
+// Estimates of the two, in SM cycles.
+double int8_gemm_cycles(long long M, long long N, long long K);
+double int8_mid_cycles(long long M, long long N, long long K);
 // Status bits their kernels left on the current device (as read_device_status).
 int read_gemm_status(int* flags, bool clear);
 int read_mid_status(int* flags, bool clear);
