@@ -121,6 +121,10 @@ __device__ __forceinline__ void reduce_row(float& a, float& b) {
     }
 }
 
+// v rounded to the nearest integer, ties to even, for |v| <= 2^22: the low bits of v + 1.5 * 2^23 (the
+// conversion instruction takes several times as long).
+__device__ __forceinline__ uint32_t round_bits(float v) { return __float_as_uint(__fadd_rn(v, 12582912.0f)); }
+
 struct RowParams {
     const void* x;
     const void* residual;
@@ -207,14 +211,22 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
         const float k = finite && a >= kTiny ? 127.0f / a : 0.0f;
         if (t == 0) p.scale[row] = !finite ? __uint_as_float(0x7fffffffu) : a >= kTiny ? a / 127.0f : 0.0f;
         int8_t* out = static_cast<int8_t*>(p.out) + row * p.out_stride;
+        const uint32_t keep = finite ? 0xffffffffu : 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (WHAT == kNormQ8) load_weight<V>(p.weight, (i * T + t) * V, n, w);
             Pack<int8_t, V> o;
+            uint32_t b[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float y = WHAT == kNormQ8 ? h[i][j] * s * w[j] : h[i][j];
-                o.e[j] = finite ? (int8_t)__float2int_rn(y * k) : (int8_t)0;
+            for (int j = 0; j < V; ++j)
+                b[j] = round_bits(__fmul_rn(WHAT == kNormQ8 ? h[i][j] * s * w[j] : h[i][j], k)) & keep;
+            if constexpr (V >= 4) {
+                uint32_t* words = reinterpret_cast<uint32_t*>(&o.word);
+#pragma unroll
+                for (int j = 0; j < V; j += 4)
+                    words[j / 4] = __byte_perm(__byte_perm(b[j], b[j + 1], 0x0040), __byte_perm(b[j + 2], b[j + 3], 0x0040), 0x5410);
+            } else {
+                o.e[0] = (int8_t)b[0];
             }
             store_pack<int8_t, V>(out, (i * T + t) * V, n, o);
         }
@@ -233,6 +245,7 @@ void pick_rows(const RowParams& p, cudaStream_t st) {
     const int n = p.cols;
     if (n <= 256) start_rows<E, WHAT, V, 32, 8>(p, st);
     else if (n <= 512) start_rows<E, WHAT, V, 32, 16>(p, st);
+    else if (n <= 768) start_rows<E, WHAT, V, 32, 24>(p, st);
     else if (n <= 1024) start_rows<E, WHAT, V, 32, 32>(p, st);
     else if (n <= 2048) start_rows<E, WHAT, V, 128, 16>(p, st);
     else if (n <= 4096) start_rows<E, WHAT, V, 128, 32>(p, st);
@@ -280,18 +293,19 @@ struct GradParams {
     float eps;
 };
 
-// A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; thread t keeps the
-// sums of dweight for its columns in registers and the CTA writes them as one
-// partial row at the end.
+// T threads take a row, T = 32 eight rows to a CTA at a time, which goes
+// through the matrix with the grid's stride; thread t keeps the sums of dweight
+// for its columns in registers, and the CTA writes them as one partial row.
 template <typename E, int V, int T, int NV>
-__global__ void __launch_bounds__(T) grad_kernel(const GradParams p) {
-    const int t = threadIdx.x, n = p.cols;
+__global__ void __launch_bounds__(kThreads<T>, T == 32 ? 2 : 1) grad_kernel(const GradParams p) {
+    constexpr int R = kThreads<T> / T;
+    const int t = threadIdx.x % T, n = p.cols;
     float acc[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (long long row = (long long)blockIdx.x * R + threadIdx.x / T; row < p.rows; row += (long long)gridDim.x * R) {
         const E* dy = static_cast<const E*>(p.dy) + row * p.dy_stride;
         const E* h = static_cast<const E*>(p.h) + row * p.h_stride;
         Pack<E, V> py[NV], ph[NV], pr[NV];
@@ -335,8 +349,28 @@ __global__ void __launch_bounds__(T) grad_kernel(const GradParams p) {
             store_pack<E, V>(dx, (i * T + t) * V, n, o);
         }
     }
-    if (p.partial != nullptr) {
-        float* part = p.partial + (long long)blockIdx.x * n;
+    if (p.partial == nullptr) return;
+    float* part = p.partial + (long long)blockIdx.x * n;
+    if constexpr (R > 1) {
+        // the CTA's rows of sums, one after the other
+        __shared__ float sums[NV * V * T];
+        for (int r = 0; r < R; ++r) {
+            if (threadIdx.x / T == r) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        float* at = &sums[(i * V + j) * T + t];   // a bank for each thread
+                        *at = r == 0 ? acc[i][j] : *at + acc[i][j];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < n; c += kThreads<T>) {
+            const int i = c / (T * V), j = c % V;
+            part[c] = sums[(i * V + j) * T + c / V % T];
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -351,10 +385,13 @@ __global__ void __launch_bounds__(T) grad_kernel(const GradParams p) {
 // each summing every 32nd partial in order, then the 32 sums in order.
 __global__ void __launch_bounds__(1024) grad_sum_kernel(const float* partial, float* dweight, int parts, int cols) {
     __shared__ float sm[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are the kernel's before
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.0f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 5
         for (int r = threadIdx.y; r < parts; r += 32) v += partial[(long long)r * cols + c];
+    }
     sm[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && c < cols) {
@@ -364,16 +401,22 @@ __global__ void __launch_bounds__(1024) grad_sum_kernel(const float* partial, fl
     }
 }
 
+template <typename E, int V, int T, int EPT>
+void start_grad(const GradParams& p, int parts, cudaStream_t st) {
+    grad_kernel<E, V, T, EPT / V><<<parts, kThreads<T>, 0, st>>>(p);
+}
+
 template <typename E, int V>
 void pick_grad(const GradParams& p, int parts, cudaStream_t st) {
     const int n = p.cols;
-    if (n <= 512) grad_kernel<E, V, 64, 8 / V><<<parts, 64, 0, st>>>(p);
-    else if (n <= 1024) grad_kernel<E, V, 128, 8 / V><<<parts, 128, 0, st>>>(p);
-    else if (n <= 2048) grad_kernel<E, V, 128, 16 / V><<<parts, 128, 0, st>>>(p);
-    else if (n <= 4096) grad_kernel<E, V, 256, 16 / V><<<parts, 256, 0, st>>>(p);
-    else if (n <= 8192) grad_kernel<E, V, 512, 16 / V><<<parts, 512, 0, st>>>(p);
-    else if (n <= 16384) grad_kernel<E, V, 1024, 16 / V><<<parts, 1024, 0, st>>>(p);
-    else grad_kernel<E, V, 1024, 32 / V><<<parts, 1024, 0, st>>>(p);
+    if (n <= 256) start_grad<E, V, 32, 8>(p, parts, st);
+    else if (n <= 512) start_grad<E, V, 32, 16>(p, parts, st);
+    else if (n <= 1024) start_grad<E, V, 32, 32>(p, parts, st);
+    else if (n <= 2048) start_grad<E, V, 128, 16>(p, parts, st);
+    else if (n <= 4096) start_grad<E, V, 256, 16>(p, parts, st);
+    else if (n <= 8192) start_grad<E, V, 512, 16>(p, parts, st);
+    else if (n <= 16384) start_grad<E, V, 1024, 16>(p, parts, st);
+    else start_grad<E, V, 1024, 32>(p, parts, st);
 }
 
 template <typename E>
@@ -386,42 +429,68 @@ void type_grad(const GradParams& p, int parts, cudaStream_t st) {
     else pick_grad<E, 1>(p, parts, st);
 }
 
-// 16 values of a row to a thread.
+// A warp takes kSpan values of a row, V to a lane at a time, the loads first.
+constexpr int kSpan = 1024;
 template <typename E, int V>
-__global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, const float* scale, E* out, long long rows,
-                                                      long long q_stride, long long out_stride, int cols) {
-    const int packs = (cols + V - 1) / V;
-    const long long all = rows * packs, step = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += step) {
-        const long long row = i / packs;
-        const int c = (int)(i - row * packs) * V;
-        const float s = scale[row];
-        const int8_t* src = q + row * q_stride;
-        E* dst = out + row * out_stride;
-        if (c + V <= cols) {
-            Pack<int8_t, V> in;
-            in.word = *reinterpret_cast<const typename Word<V>::T*>(src + c);
-            Pack<E, V> o;
+__global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, const float* scale, E* out, unsigned spans,
+                                                      long long q_stride, long long out_stride, int cols,
+                                                      unsigned spans_a_row) {
+    constexpr int NV = V == 1 ? 4 : kSpan / (32 * V), LOOPS = kSpan / (32 * V * NV);
+    const unsigned span = blockIdx.x * 8u + (threadIdx.x >> 5);
+    if (span >= spans) return;
+    const unsigned row = span / spans_a_row;
+    const int c0 = (int)(span - row * spans_a_row) * kSpan, lane = threadIdx.x & 31;
+    const float s = scale[row];
+    const int8_t* src = q + row * q_stride;
+    E* dst = out + row * out_stride;
+    for (int l = 0; l < LOOPS; ++l) {
+        Pack<int8_t, V> in[NV];
 #pragma unroll
-            for (int j = 0; j < V; ++j) o.e[j] = from_f<E>((float)in.e[j] * s);
-            *reinterpret_cast<typename Word<sizeof(E) * V>::T*>(dst + c) = o.word;
-        } else {
-            for (int j = c; j < cols; ++j) dst[j] = from_f<E>((float)src[j] * s);
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + ((l * NV + i) * 32 + lane) * V;
+            if (c + V <= cols) in[i].word = *reinterpret_cast<const typename Word<V>::T*>(src + c);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + ((l * NV + i) * 32 + lane) * V;
+            if (c + V <= cols) {
+                Pack<E, V> o;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    // the byte u = q + 128 as 2^23 + u, exactly
+                    const uint32_t u = (uint32_t)(uint8_t)in[i].e[j] ^ 0x80u;
+                    o.e[j] = from_f<E>((__uint_as_float(0x4B000000u | u) - 8388736.0f) * s);
+                }
+                *reinterpret_cast<typename Word<sizeof(E) * V>::T*>(dst + c) = o.word;
+            } else {
+                for (int j = c; j < cols; ++j) dst[j] = from_f<E>((float)src[j] * s);
+            }
         }
     }
 }
 
 template <typename E>
-void type_dequant(const DequantArgs& a, cudaStream_t st) {
+int type_dequant(const DequantArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(E);
     const bool wide = on_pack(a.q, a.q_stride, 1, V, a.rows) && on_pack(a.out, a.out_stride, sizeof(E), V, a.rows);
-    const long long packs = a.rows * ((a.cols + (wide ? V : 1) - 1) / (wide ? V : 1));
-    const unsigned grid = (unsigned)((packs + 255) / 256 < (1 << 30) ? (packs + 255) / 256 : (1 << 30));
-    E* out = static_cast<E*>(a.out);
-    if (wide)
-        dequant_kernel<E, V><<<grid, 256, 0, st>>>(a.q, a.scale, out, a.rows, a.q_stride, a.out_stride, a.cols);
-    else
-        dequant_kernel<E, 1><<<grid, 256, 0, st>>>(a.q, a.scale, out, a.rows, a.q_stride, a.out_stride, a.cols);
+    const long long spans_a_row = (a.cols + kSpan - 1) / kSpan;
+    // rows beyond a grid's reach in further launches
+    for (long long r0 = 0; r0 < a.rows;) {
+        const long long most = (1LL << 31) / spans_a_row, rows = a.rows - r0 < most ? a.rows - r0 : most;
+        const unsigned spans = (unsigned)(rows * spans_a_row), grid = (spans + 7) / 8;
+        const int8_t* q = a.q + r0 * a.q_stride;
+        E* out = static_cast<E*>(a.out) + r0 * a.out_stride;
+        if (wide)
+            dequant_kernel<E, V><<<grid, 256, 0, st>>>(q, a.scale + r0, out, spans, a.q_stride, a.out_stride, a.cols,
+                                                       (unsigned)spans_a_row);
+        else
+            dequant_kernel<E, 1><<<grid, 256, 0, st>>>(q, a.scale + r0, out, spans, a.q_stride, a.out_stride, a.cols,
+                                                       (unsigned)spans_a_row);
+        const int rc = launched("dequantisation kernel");
+        if (rc != TR_OK) return rc;
+        r0 += rows;
+    }
+    return TR_OK;
 }
 
 }  // namespace
@@ -437,9 +506,11 @@ int launch_rows(const RowArgs& a) {
 }
 
 int row_grad_parts(long long rows, long long cols) {
-    // two CTAs for each of 152 SMs' worth of columns, a row each at least
-    const long long want = cols <= 2048 ? 152 * 8 : cols <= 8192 ? 152 * 4 : 152;
-    return (int)(rows < want ? (rows < 1 ? 1 : rows) : want);
+    // the CTAs that 152 SMs hold at once, a row for each thread group at least
+    const long long per = cols <= 1024 ? 8 : 1;
+    const long long want = 152 * (cols <= 1024 ? 2 : cols <= 2048 ? 8 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1);
+    const long long most = (rows + per - 1) / per;
+    return (int)(most < want ? (most < 1 ? 1 : most) : want);
 }
 
 int launch_row_grad(const RowGradArgs& a) {
@@ -452,16 +523,29 @@ int launch_row_grad(const RowGradArgs& a) {
     else type_grad<__nv_bfloat16>(p, parts, st);
     int rc = launched("row gradient kernel");
     if (rc != TR_OK || a.dweight == nullptr) return rc;
-    grad_sum_kernel<<<(a.cols + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, a.dweight, parts, a.cols);
+    // its start overlaps the end of the kernel that it waits for
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.cols + 31) / 32));
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_sum_kernel, (const float*)a.partial, a.dweight, parts, a.cols);
+    if (e != cudaSuccess) {
+        set_last_error("cudaLaunchKernelEx(weight gradient sum)", (int)e);
+        return TR_ERR_CUDA;
+    }
     return launched("weight gradient sum kernel");
 }
 
 int launch_dequant(const DequantArgs& a) {
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-    if (a.dtype == TR_ELEM_F32) type_dequant<float>(a, st);
-    else if (a.dtype == TR_ELEM_F16) type_dequant<__half>(a, st);
-    else type_dequant<__nv_bfloat16>(a, st);
-    return launched("dequantisation kernel");
+    if (a.dtype == TR_ELEM_F32) return type_dequant<float>(a, st);
+    if (a.dtype == TR_ELEM_F16) return type_dequant<__half>(a, st);
+    return type_dequant<__nv_bfloat16>(a, st);
 }
 
 }  // namespace trfn
