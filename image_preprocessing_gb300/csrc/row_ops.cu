@@ -11,6 +11,12 @@
 // All of them are bound by HBM: a row is read once, kept in registers, reduced
 // once, and written.  max_c |y_c| = s max_c |h_c w_c| needs no s, so the 8-bit
 // output takes one reduction, of the pair (sum of squares, maximum).
+//
+// Rows are accessed in packs of 16 bytes.  Where a row's length is odd, its
+// rows start off the 16-byte boundaries, but all matrices of a call alike
+// (the usual case: equal strides, aligned buffers): then row r starts
+// s = r * stride mod V values into a pack, and lane i's pack holds columns
+// i V - s ... (SHIFT).  Any other alignment goes value by value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,33 +51,67 @@ union Pack {
     __device__ __forceinline__ Pack() {}
 };
 
-// Values c .. c+V-1 of a row of n, zeros past its end.  V > 1 only where every
-// row starts on a boundary of the access.
+// Values c .. c+V-1 of a row of n, zeros outside 0 .. n-1.  V > 1 only where
+// the row's value c lies on a boundary of the access.  `over`: the bytes next to
+// the row, up to the boundary, belong to the matrix too and may be read (they
+// are not used).
 template <typename E, int V>
-__device__ __forceinline__ Pack<E, V> load_pack(const E* row, int c, int n) {
+__device__ __forceinline__ Pack<E, V> load_pack(const E* row, int c, int n, bool over) {
     Pack<E, V> p;
-    if (c + V <= n) {
+    const bool whole = c >= 0 && c + V <= n;
+    if (whole || (over && c < n)) {
         p.word = *reinterpret_cast<const typename Word<sizeof(E) * V>::T*>(row + c);
+        if (!whole)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (c + j < 0 || c + j >= n) p.e[j] = from_f<E>(0.0f);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) p.e[j] = (c + j < n) ? row[c + j] : from_f<E>(0.0f);
+        for (int j = 0; j < V; ++j) p.e[j] = (c + j >= 0 && c + j < n) ? row[c + j] : from_f<E>(0.0f);
     }
     return p;
+}
+// Whether packs of row `row` may be read over its ends: another row lies beyond (a stride below a pack, as of
+// one row that is repeated, says no).
+__device__ __forceinline__ bool may_over(long long row, long long rows, long long stride, int V) {
+    return row + 1 < rows && stride >= V;
 }
 
 template <typename E, int V>
 __device__ __forceinline__ void store_pack(E* row, int c, int n, const Pack<E, V>& p) {
-    if (c + V <= n) {
+    if (c >= 0 && c + V <= n) {
         *reinterpret_cast<typename Word<sizeof(E) * V>::T*>(row + c) = p.word;
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (c + j < n) row[c + j] = p.e[j];
+            if (c + j >= 0 && c + j < n) row[c + j] = p.e[j];
     }
 }
 
+// Weights of shifted packs lie in shared memory as V rows: value c at row c mod V, place c / V + 1, zeros
+// around them.  The j-th values of the lanes' packs are then neighbours in one row, without bounds to look at.
+constexpr int kShiftCols = 8192;   // rows with shifted packs are this long at most
+template <int V> __host__ __device__ constexpr int shift_pitch(int cols) { return cols / V + 3; }
+
 template <int V>
-__device__ __forceinline__ void load_weight(const float* w, int c, int n, float (&v)[V]) {
+__device__ __forceinline__ void share_weight(const float* w, float* shared, int n) {
+    const int pitch = shift_pitch<V>(n);
+    for (int i = threadIdx.x; i < V * pitch; i += blockDim.x) {
+        const int c = (i % pitch - 1) * V + i / pitch;
+        shared[i] = c >= 0 && c < n ? (w != nullptr ? w[c] : 1.0f) : 0.0f;
+    }
+}
+
+// Weights of the pack that starts at column c = pack * V - s, s < V.  (Packs past the row's end read the last
+// place: their values are not used.)
+template <int V, bool SHIFT>
+__device__ __forceinline__ void load_weight(const float* w, const float* shared, int c, int pack, int s, int n, float (&v)[V]) {
+    if constexpr (SHIFT) {
+        const int place = min(pack, shift_pitch<V>(n) - 2);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = shared[((j - s) & (V - 1)) * shift_pitch<V>(n) + (j < s ? 0 : 1) + place];
+        return;
+    }
     if (w == nullptr) {
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = 1.0f;
@@ -141,38 +181,41 @@ struct RowParams {
 template <int T> constexpr int kThreads = T == 32 ? 256 : T;
 
 // T threads take a row, thread i the packs i, i + T, ... (NV of them).
-template <typename E, RowWhat WHAT, int V, int T, int NV>
+template <typename E, RowWhat WHAT, int V, int T, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
+    extern __shared__ float shared_weight[];   // with SHIFT
     const int t = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
     const long long row = T == 32 ? (long long)blockIdx.x * (kThreads<T> / 32) + (threadIdx.x >> 5) : blockIdx.x;
-    if (T == 32 && row >= p.rows) return;
-    const int n = p.cols;
+    const bool some = T > 32 || row < p.rows;
+    if (!SHIFT && !some) return;
+    const int n = some ? p.cols : 0, shift = SHIFT ? (int)((row * p.x_stride) & (V - 1)) : 0, c0 = t * V - shift;
     const E* x = static_cast<const E*>(p.x) + row * p.x_stride;
-    Pack<E, V> px[NV];
+    Pack<E, V> px[NV], pr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) px[i] = load_pack<E, V>(x, i * T * V + c0, n, SHIFT && may_over(row, p.rows, p.x_stride, V));
+    const bool add = WHAT != kQuantize && p.residual != nullptr;
+    if (add) {
+        const E* r = static_cast<const E*>(p.residual) + row * p.residual_stride;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            pr[i] = load_pack<E, V>(r, i * T * V + c0, n, SHIFT && may_over(row, p.rows, p.residual_stride, V));
+    }
+    if constexpr (SHIFT && WHAT != kQuantize) {   // while the rows are on their way
+        share_weight<V>(p.weight, shared_weight, p.cols);
+        __syncthreads();
+    }
+    if (!some) return;
     float h[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) px[i] = load_pack<E, V>(x, (i * T + t) * V, n);
-    if (WHAT != kQuantize && p.residual != nullptr) {
-        const E* r = static_cast<const E*>(p.residual) + row * p.residual_stride;
-        Pack<E, V> pr[NV];
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) pr[i] = load_pack<E, V>(r, (i * T + t) * V, n);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) h[i][j] = to_f(px[i].e[j]) + to_f(pr[i].e[j]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) h[i][j] = to_f(px[i].e[j]);
-    }
+        for (int j = 0; j < V; ++j) h[i][j] = add ? to_f(px[i].e[j]) + to_f(pr[i].e[j]) : to_f(px[i].e[j]);
     float sum = 0.0f;
     unsigned top = 0;   // |.| as bits: orders like the values, infinities and NaN on top
     float w[V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (WHAT == kNormQ8) load_weight<V>(p.weight, (i * T + t) * V, n, w);
+        if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (WHAT != kQuantize) sum = fmaf(h[i][j], h[i][j], sum);
@@ -192,18 +235,18 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
             Pack<E, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) o.e[j] = from_f<E>(h[i][j]);
-            store_pack<E, V>(ho, (i * T + t) * V, n, o);
+            store_pack<E, V>(ho, i * T * V + c0, n, o);
         }
     }
     if constexpr (WHAT == kNorm) {
         E* out = static_cast<E*>(p.out) + row * p.out_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            load_weight<V>(p.weight, (i * T + t) * V, n, w);
+            load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
             Pack<E, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) o.e[j] = from_f<E>(h[i][j] * s * w[j]);
-            store_pack<E, V>(out, (i * T + t) * V, n, o);
+            store_pack<E, V>(out, i * T * V + c0, n, o);
         }
     } else {
         const float a = __float_as_uint(ftop) >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : s * ftop;
@@ -214,7 +257,7 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
         const uint32_t keep = finite ? 0xffffffffu : 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (WHAT == kNormQ8) load_weight<V>(p.weight, (i * T + t) * V, n, w);
+            if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
             Pack<int8_t, V> o;
             uint32_t b[V];
 #pragma unroll
@@ -228,50 +271,66 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
             } else {
                 o.e[0] = (int8_t)b[0];
             }
-            store_pack<int8_t, V>(out, (i * T + t) * V, n, o);
+            store_pack<int8_t, V>(out, i * T * V + c0, n, o);
         }
     }
 }
 
-template <typename E, RowWhat WHAT, int V, int T, int EPT>
+
+template <typename E, RowWhat WHAT, int V, int T, int EPT, bool SHIFT>
 void start_rows(const RowParams& p, cudaStream_t st) {
     const long long per = kThreads<T> / T;
-    row_kernel<E, WHAT, V, T, EPT / V><<<(unsigned)((p.rows + per - 1) / per), kThreads<T>, 0, st>>>(p);
+    row_kernel<E, WHAT, V, T, EPT / V, SHIFT>
+        <<<(unsigned)((p.rows + per - 1) / per), kThreads<T>, SHIFT && WHAT != kQuantize ? V * shift_pitch<V>(p.cols) * sizeof(float) : 0, st>>>(p);
 }
 
 // Threads for a row, and values for a thread, by the row's length alone.
-template <typename E, RowWhat WHAT, int V>
+template <typename E, RowWhat WHAT, int V, bool SHIFT>
 void pick_rows(const RowParams& p, cudaStream_t st) {
-    const int n = p.cols;
-    if (n <= 256) start_rows<E, WHAT, V, 32, 8>(p, st);
-    else if (n <= 512) start_rows<E, WHAT, V, 32, 16>(p, st);
-    else if (n <= 768) start_rows<E, WHAT, V, 32, 24>(p, st);
-    else if (n <= 1024) start_rows<E, WHAT, V, 32, 32>(p, st);
-    else if (n <= 2048) start_rows<E, WHAT, V, 128, 16>(p, st);
-    else if (n <= 4096) start_rows<E, WHAT, V, 128, 32>(p, st);
-    else if (n <= 8192) start_rows<E, WHAT, V, 256, 32>(p, st);
-    else if (n <= 16384) start_rows<E, WHAT, V, 512, 32>(p, st);
-    else start_rows<E, WHAT, V, 1024, 32>(p, st);
+    const int n = p.cols + (SHIFT ? V - 1 : 0);
+    if (n <= 256) start_rows<E, WHAT, V, 32, 8, SHIFT>(p, st);
+    else if (n <= 512) start_rows<E, WHAT, V, 32, 16, SHIFT>(p, st);
+    else if (n <= 768) start_rows<E, WHAT, V, 32, 24, SHIFT>(p, st);
+    else if (n <= 1024) start_rows<E, WHAT, V, 32, 32, SHIFT>(p, st);
+    else if (n <= 2048) start_rows<E, WHAT, V, 128, 16, SHIFT>(p, st);
+    else if (n <= 128 * 24) start_rows<E, WHAT, V, 128, 24, SHIFT>(p, st);
+    else if (n <= 4096) start_rows<E, WHAT, V, 128, 32, SHIFT>(p, st);
+    else if (SHIFT || n <= 8192) start_rows<E, WHAT, V, SHIFT ? 512 : 256, SHIFT ? 24 : 32, SHIFT>(p, st);
+    else if constexpr (!SHIFT) {
+        if (n <= 16384) start_rows<E, WHAT, V, 512, 32, SHIFT>(p, st);
+        else start_rows<E, WHAT, V, 1024, 32, SHIFT>(p, st);
+    }
 }
 
-bool on16(const void* p, long long stride_bytes, long long rows) {
-    return (uintptr_t)p % 16 == 0 && (rows <= 1 || stride_bytes % 16 == 0);
+// How the rows of a matrix lie on packs of V values of es bytes: 0 all of them
+// on boundaries, f > 0 row r starts f r mod V values into a pack, -1 neither.
+int phase_of(const void* p, long long stride, int es, int V, long long rows) {
+    if ((uintptr_t)p % (unsigned)(es * V) != 0) return -1;
+    return rows <= 1 ? 0 : (int)(stride & (V - 1));
 }
+// The phase that all matrices of a call share, else -1.
+struct Phase {
+    int f = -2;
+    void add(const void* p, long long stride, int es, int V, long long rows) {
+        if (p == nullptr) return;
+        const int g = phase_of(p, stride, es, V, rows);
+        f = f == -2 || f == g ? g : -1;
+    }
+};
 // Whether packs of V values of es bytes can be accessed whole.
-bool on_pack(const void* p, long long stride, int es, int V, long long rows) {
-    return (uintptr_t)p % (unsigned)(es * V) == 0 && (rows <= 1 || (stride * es) % (es * V) == 0);
-}
+bool on_pack(const void* p, long long stride, int es, int V, long long rows) { return phase_of(p, stride, es, V, rows) == 0; }
 
 template <typename E, RowWhat WHAT>
 void align_rows(const RowParams& p, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(E), es = sizeof(E);
-    const bool wide = on_pack(p.x, p.x_stride, es, V, p.rows) &&
-                      (p.residual == nullptr || on_pack(p.residual, p.residual_stride, es, V, p.rows)) &&
-                      on_pack(p.out, p.out_stride, WHAT == kNorm ? es : 1, V, p.rows) &&
-                      (p.residual_out == nullptr || on_pack(p.residual_out, p.residual_out_stride, es, V, p.rows)) &&
-                      (uintptr_t)p.weight % 16 == 0;
-    if (wide) pick_rows<E, WHAT, V>(p, st);
-    else pick_rows<E, WHAT, 1>(p, st);
+    constexpr int es = sizeof(E), V = 16 / es;
+    Phase phase;
+    phase.add(p.x, p.x_stride, es, V, p.rows);
+    phase.add(p.residual, p.residual_stride, es, V, p.rows);
+    phase.add(p.out, p.out_stride, WHAT == kNorm ? es : 1, V, p.rows);
+    phase.add(p.residual_out, p.residual_out_stride, es, V, p.rows);
+    if (phase.f == 0 && (uintptr_t)p.weight % 16 == 0) pick_rows<E, WHAT, V, false>(p, st);
+    else if (phase.f >= 0 && p.cols <= kShiftCols) pick_rows<E, WHAT, V, true>(p, st);
+    else pick_rows<E, WHAT, 1, false>(p, st);
 }
 
 template <typename E>
@@ -293,91 +352,194 @@ struct GradParams {
     float eps;
 };
 
+__host__ __device__ constexpr int padded(int c) { return c + (c >> 5); }
+
+// Two binary32 values in one register pair, and the instructions that work on both.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 apart(Two v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Two mul_two(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // T threads take a row, T = 32 eight rows to a CTA at a time, which goes
-// through the matrix with the grid's stride; thread t keeps the sums of dweight
-// for its columns in registers, and the CTA writes them as one partial row.
-template <typename E, int V, int T, int NV>
-__global__ void __launch_bounds__(kThreads<T>, T == 32 ? 2 : 1) grad_kernel(const GradParams p) {
-    constexpr int R = kThreads<T> / T;
+// through the matrix with the grid's stride.  A thread's columns are the same
+// in every row, so it keeps their weights and their sums of dweight in
+// registers, and the CTA writes the sums as one partial row.  (With SHIFT the
+// columns depend on the row's place in a pack; the grid and the rows of a CTA
+// are multiples of 8, so that this stays the same too.)  With 16 columns to a
+// thread the arithmetic, about 10 instructions a value, is what competes with
+// HBM: it works on pairs of binary32.
+//
+// A thread copies its packs of the next rows into shared memory while it works
+// on this one; they are its own, so no barrier is needed.  kAhead rows ahead:
+// about 100 KB an SM under way, what its share of the HBM rate takes.
+template <int V, int T, int NV> constexpr int kRowBytes = V > 1 ? 3 * NV * 16 * kThreads<T> : 0;
+template <int V, int T, int NV>
+constexpr int kAhead = V == 1 ? 0 : (V == 8 ? 3 : 2) * kRowBytes<V, T, NV> <= 200 * 1024 ? (V == 8 ? 3 : 2) : 200 * 1024 / kRowBytes<V, T, NV>;
+
+template <typename E, int V, int T, int NV, bool SHIFT>
+__global__ void __launch_bounds__(kThreads<T>) grad_kernel(const GradParams p) {
+    constexpr int R = kThreads<T> / T, N = NV * V;   // N values to a thread
+    static_assert(N % 2 == 0, "values are taken in pairs");
+    constexpr int AHEAD = kAhead<V, T, NV>;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    uint4* const mine = reinterpret_cast<uint4*>(dynamic) + threadIdx.x;   // AHEAD x 3 NV packs, kThreads<T> apart
     const int t = threadIdx.x % T, n = p.cols;
-    float acc[NV][V];
+    const long long row0 = (long long)blockIdx.x * R + threadIdx.x / T, step = (long long)gridDim.x * R;
+    const int c0 = t * V - (SHIFT ? (int)((row0 * p.h_stride) & (V - 1)) : 0);
+    auto column = [&](int e) { return e / V * (T * V) + c0 + e % V; };
+    auto in_row = [&](int e) { return column(e) >= 0 && column(e) < n; };
+    // packs inside the row, and (SHIFT) those across its ends, which are read whole but in the last row
+    bool inside[NV], across[NV];
+    const bool strides_over = p.dy_stride >= V && p.h_stride >= V && (p.dresidual == nullptr || p.dresidual_stride >= V);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * T * V + c0;
+        inside[i] = c >= 0 && c + V <= n;
+        across[i] = SHIFT && strides_over && !inside[i] && c < n;
+    }
+    const E* dy_next = static_cast<const E*>(p.dy) + row0 * p.dy_stride + c0;
+    const E* h_next = static_cast<const E*>(p.h) + row0 * p.h_stride + c0;
+    const E* r_next = static_cast<const E*>(p.dresidual) + (p.dresidual != nullptr ? row0 * p.dresidual_stride + c0 : 0);
+    long long row_next = row0;
+    auto fetch = [&](int slot) {
+        if constexpr (AHEAD > 0) {
+            if (row_next < p.rows) {
+                const bool over = row_next + 1 < p.rows;
+                uint32_t to = (uint32_t)__cvta_generic_to_shared(mine) + slot * (3 * NV * 16 * kThreads<T>);
+                auto one = [&](const E* from) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
-    for (long long row = (long long)blockIdx.x * R + threadIdx.x / T; row < p.rows; row += (long long)gridDim.x * R) {
-        const E* dy = static_cast<const E*>(p.dy) + row * p.dy_stride;
-        const E* h = static_cast<const E*>(p.h) + row * p.h_stride;
-        Pack<E, V> py[NV], ph[NV], pr[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            py[i] = load_pack<E, V>(dy, (i * T + t) * V, n);
-            ph[i] = load_pack<E, V>(h, (i * T + t) * V, n);
+                    for (int i = 0; i < NV; ++i)
+                        if (inside[i] || (across[i] && over))
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * (16 * kThreads<T>)),
+                                         "l"(from + i * T * V)
+                                         : "memory");
+                    to += NV * 16 * kThreads<T>;
+                };
+                one(dy_next);
+                one(h_next);
+                if (p.dresidual != nullptr) one(r_next);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            row_next += step;
+            dy_next += step * p.dy_stride;
+            h_next += step * p.h_stride;
+            if (p.dresidual != nullptr) r_next += step * p.dresidual_stride;
         }
-        if (p.dresidual != nullptr) {
-            const E* r = static_cast<const E*>(p.dresidual) + row * p.dresidual_stride;
+    };
+    // a pack that was copied, or one across an end of the last row
+    auto take = [&](const void* base, long long stride, int m, int i, long long row, bool over, int slot) {
+        const int c = i * T * V + c0;
+        if constexpr (AHEAD > 0) {
+            if (inside[i] || (across[i] && over)) {
+                Pack<E, V> pack;
+                *reinterpret_cast<uint4*>(&pack.word) = mine[((slot * 3 + m) * NV + i) * kThreads<T>];
+                if (SHIFT && !inside[i])
 #pragma unroll
-            for (int i = 0; i < NV; ++i) pr[i] = load_pack<E, V>(r, (i * T + t) * V, n);
-        }
-        float hh = 0.0f, gh = 0.0f, w[V];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            load_weight<V>(p.weight, (i * T + t) * V, n, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float hv = to_f(ph[i].e[j]);
-                hh = fmaf(hv, hv, hh);
-                gh = fmaf(to_f(py[i].e[j]) * w[j], hv, gh);
+                    for (int j = 0; j < V; ++j)
+                        if (c + j < 0 || c + j >= n) pack.e[j] = from_f<E>(0.0f);
+                return pack;
             }
         }
-        reduce_row<T, false>(hh, gh);
-        const float s = rsqrtf(hh / (float)n + p.eps);
-        const float along = gh / (float)n * s * s;
-        E* dx = static_cast<E*>(p.dx) + row * p.dx_stride;
+        return load_pack<E, V>(static_cast<const E*>(base) + row * stride, c, n, false);
+    };
+    Two acc[N / 2], w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        acc[e / 2] = two(0.0f, 0.0f);
+        w[e / 2] = two(p.weight != nullptr && in_row(e) ? p.weight[column(e)] : 1.0f,
+                       p.weight != nullptr && in_row(e + 1) ? p.weight[column(e + 1)] : 1.0f);
+    }
+    for (int a = 0; a < AHEAD; ++a) fetch(a);
+    E* dx = static_cast<E*>(p.dx) + row0 * p.dx_stride;
+    int slot = 0;
+    for (long long row = row0; row < p.rows; row += step) {
+        const bool over = row + 1 < p.rows;
+        Pack<E, V> py[NV], ph[NV], pr[NV];
+        if constexpr (AHEAD > 0) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            load_weight<V>(p.weight, (i * T + t) * V, n, w);
+            py[i] = take(p.dy, p.dy_stride, 0, i, row, over, slot);
+            ph[i] = take(p.h, p.h_stride, 1, i, row, over, slot);
+            if (p.dresidual != nullptr) pr[i] = take(p.dresidual, p.dresidual_stride, 2, i, row, over, slot);
+        }
+        auto pair = [&](const Pack<E, V> (&v)[NV], int e) {
+            return two(to_f(v[e / V].e[e % V]), to_f(v[(e + 1) / V].e[(e + 1) % V]));
+        };
+        Two hh2 = two(0.0f, 0.0f), gh2 = two(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const Two h = pair(ph, e);
+            hh2 = fma_two(h, h, hh2);
+            gh2 = fma_two(mul_two(pair(py, e), w[e / 2]), h, gh2);
+        }
+        fetch(slot);   // the packs are in registers
+        if (++slot >= AHEAD) slot = 0;
+        float hh = apart(hh2).x + apart(hh2).y, gh = apart(gh2).x + apart(gh2).y;
+        reduce_row<T, false>(hh, gh);
+        // dx = s g - (s^3 gh / n) h + dres
+        const float s = rsqrtf(hh / (float)n + p.eps), along = -(gh / (float)n * s * s * s);
+        const Two s2 = two(s, s), along2 = two(along, along);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
             Pack<E, V> o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float hv = to_f(ph[i].e[j]), yv = to_f(py[i].e[j]);
-                float d = s * (yv * w[j] - hv * along);
-                if (p.dresidual != nullptr) d += to_f(pr[i].e[j]);
-                o.e[j] = from_f<E>(d);
-                acc[i][j] = fmaf(yv, hv * s, acc[i][j]);
+            for (int j = 0; j < V; j += 2) {
+                // (V = 1: pairs are of two packs; the second pack's half is made with it)
+                const int e = V > 1 ? i * V + j : i / 2 * 2;
+                const Two h = pair(ph, e), y = pair(py, e);
+                const Two r = p.dresidual != nullptr ? pair(pr, e) : two(0.0f, 0.0f);
+                const float2 d = apart(fma_two(s2, mul_two(y, w[e / 2]), fma_two(along2, h, r)));
+                if constexpr (V > 1) {
+                    o.e[j] = from_f<E>(d.x);
+                    o.e[j + 1] = from_f<E>(d.y);
+                    acc[e / 2] = fma_two(y, mul_two(h, s2), acc[e / 2]);
+                } else {
+                    o.e[0] = from_f<E>(i % 2 ? d.y : d.x);
+                    if (i % 2 == 0) acc[e / 2] = fma_two(y, mul_two(h, s2), acc[e / 2]);
+                }
             }
-            store_pack<E, V>(dx, (i * T + t) * V, n, o);
+            store_pack<E, V>(dx, i * T * V + c0, n, o);
         }
+        dx += step * p.dx_stride;
     }
     if (p.partial == nullptr) return;
     float* part = p.partial + (long long)blockIdx.x * n;
     if constexpr (R > 1) {
-        // the CTA's rows of sums, one after the other
-        __shared__ float sums[NV * V * T];
-        for (int r = 0; r < R; ++r) {
-            if (threadIdx.x / T == r) {
+        // the sums of the CTA's row groups, one after the other
+        // (place c + c / 32: the threads' values, V columns apart, in different banks)
+        __shared__ float sums[padded(N * T)];
+        for (int g = 0; g < R; ++g) {
+            if (threadIdx.x / T == g) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        float* at = &sums[(i * V + j) * T + t];   // a bank for each thread
-                        *at = r == 0 ? acc[i][j] : *at + acc[i][j];
-                    }
+                for (int e = 0; e < N; ++e) {
+                    const float v = e % 2 ? apart(acc[e / 2]).y : apart(acc[e / 2]).x;
+                    if (in_row(e)) sums[padded(column(e))] = g == 0 ? v : sums[padded(column(e))] + v;
+                }
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < n; c += kThreads<T>) {
-            const int i = c / (T * V), j = c % V;
-            part[c] = sums[(i * V + j) * T + c / V % T];
-        }
+        for (int c = threadIdx.x; c < n; c += kThreads<T>) part[c] = sums[padded(c)];
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (i * T + t) * V + j;
-                if (c < n) part[c] = acc[i][j];
-            }
+        for (int e = 0; e < N; ++e)
+            if (in_row(e)) part[column(e)] = e % 2 ? apart(acc[e / 2]).y : apart(acc[e / 2]).x;
     }
 }
 
@@ -401,32 +563,47 @@ __global__ void __launch_bounds__(1024) grad_sum_kernel(const float* partial, fl
     }
 }
 
-template <typename E, int V, int T, int EPT>
-void start_grad(const GradParams& p, int parts, cudaStream_t st) {
-    grad_kernel<E, V, T, EPT / V><<<parts, kThreads<T>, 0, st>>>(p);
+template <typename E, int V, int T, int EPT, bool SHIFT>
+int start_grad(const GradParams& p, int parts, cudaStream_t st) {
+    constexpr int NV = EPT / V;
+    const size_t smem = (size_t)kAhead<V, T, NV> * kRowBytes<V, T, NV>;
+    if (smem > 40 * 1024) {   // with the static part, beyond what needs no opt-in
+        const cudaError_t e = cudaFuncSetAttribute(grad_kernel<E, V, T, NV, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem);
+        if (e != cudaSuccess) {
+            set_last_error("row gradient kernel set-up", (int)e);
+            return TR_ERR_CUDA;
+        }
+    }
+    grad_kernel<E, V, T, NV, SHIFT><<<parts, kThreads<T>, smem, st>>>(p);
+    return launched("row gradient kernel");
 }
 
-template <typename E, int V>
-void pick_grad(const GradParams& p, int parts, cudaStream_t st) {
-    const int n = p.cols;
-    if (n <= 256) start_grad<E, V, 32, 8>(p, parts, st);
-    else if (n <= 512) start_grad<E, V, 32, 16>(p, parts, st);
-    else if (n <= 1024) start_grad<E, V, 32, 32>(p, parts, st);
-    else if (n <= 2048) start_grad<E, V, 128, 16>(p, parts, st);
-    else if (n <= 4096) start_grad<E, V, 256, 16>(p, parts, st);
-    else if (n <= 8192) start_grad<E, V, 512, 16>(p, parts, st);
-    else if (n <= 16384) start_grad<E, V, 1024, 16>(p, parts, st);
-    else start_grad<E, V, 1024, 32>(p, parts, st);
+template <typename E, int V, bool SHIFT>
+int pick_grad(const GradParams& p, int parts, cudaStream_t st) {
+    const int n = p.cols + (SHIFT ? V - 1 : 0);
+    if (n <= 256) return start_grad<E, V, 32, 8, SHIFT>(p, parts, st);
+    if (n <= 512) return start_grad<E, V, 32, 16, SHIFT>(p, parts, st);
+    if (n <= 1024) return start_grad<E, V, 64, 16, SHIFT>(p, parts, st);
+    if (n <= 2048) return start_grad<E, V, 128, 16, SHIFT>(p, parts, st);
+    if (n <= 4096) return start_grad<E, V, 256, 16, SHIFT>(p, parts, st);
+    if (n <= 8192) return start_grad<E, V, 512, 16, SHIFT>(p, parts, st);
+    if (SHIFT || n <= 16384) return start_grad<E, V, 1024, 16, SHIFT>(p, parts, st);
+    if constexpr (!SHIFT) return start_grad<E, V, 1024, 32, SHIFT>(p, parts, st);
+    return TR_ERR_NOT_SUPPORTED;   // not reached
 }
 
 template <typename E>
-void type_grad(const GradParams& p, int parts, cudaStream_t st) {
-    constexpr int es = sizeof(E);
-    const bool wide = on16(p.dy, p.dy_stride * es, p.rows) && on16(p.h, p.h_stride * es, p.rows) &&
-                      (p.dresidual == nullptr || on16(p.dresidual, p.dresidual_stride * es, p.rows)) &&
-                      on16(p.dx, p.dx_stride * es, p.rows) && (uintptr_t)p.weight % 16 == 0;
-    if (wide) pick_grad<E, 16 / es>(p, parts, st);
-    else pick_grad<E, 1>(p, parts, st);
+int type_grad(const GradParams& p, int parts, cudaStream_t st) {
+    constexpr int es = sizeof(E), V = 16 / es;
+    Phase phase;
+    phase.add(p.dy, p.dy_stride, es, V, p.rows);
+    phase.add(p.h, p.h_stride, es, V, p.rows);
+    phase.add(p.dresidual, p.dresidual_stride, es, V, p.rows);
+    phase.add(p.dx, p.dx_stride, es, V, p.rows);
+    if (phase.f == 0 && (uintptr_t)p.weight % 16 == 0) return pick_grad<E, V, false>(p, parts, st);
+    if (phase.f >= 0 && p.cols <= kShiftCols) return pick_grad<E, V, true>(p, parts, st);
+    return pick_grad<E, 1, false>(p, parts, st);
 }
 
 // A warp takes kSpan values of a row, V to a lane at a time, the loads first.
@@ -506,11 +683,12 @@ int launch_rows(const RowArgs& a) {
 }
 
 int row_grad_parts(long long rows, long long cols) {
-    // the CTAs that 152 SMs hold at once, a row for each thread group at least
-    const long long per = cols <= 1024 ? 8 : 1;
-    const long long want = 152 * (cols <= 1024 ? 2 : cols <= 2048 ? 8 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1);
-    const long long most = (rows + per - 1) / per;
-    return (int)(most < want ? (most < 1 ? 1 : most) : want);
+    // the CTAs that 152 SMs hold at once, a row for each of their row groups at least; a multiple of 8, so that
+    // the rows of one are all at the same place in a pack
+    const long long per = cols <= 512 ? 8 : 1;
+    const long long want = 152 * (cols <= 512 ? 2 : cols <= 1024 ? 6 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1);
+    const long long most = ((rows + per - 1) / per + 7) / 8 * 8;
+    return (int)(most < want ? (most < 1 ? 8 : most) : want);
 }
 
 int launch_row_grad(const RowGradArgs& a) {
@@ -518,10 +696,9 @@ int launch_row_grad(const RowGradArgs& a) {
                  a.dy_stride, a.h_stride, a.dresidual_stride, a.dx_stride, a.cols, a.eps};
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     const int parts = row_grad_parts(a.rows, a.cols);
-    if (a.dtype == TR_ELEM_F32) type_grad<float>(p, parts, st);
-    else if (a.dtype == TR_ELEM_F16) type_grad<__half>(p, parts, st);
-    else type_grad<__nv_bfloat16>(p, parts, st);
-    int rc = launched("row gradient kernel");
+    const int rc = a.dtype == TR_ELEM_F32   ? type_grad<float>(p, parts, st)
+                   : a.dtype == TR_ELEM_F16 ? type_grad<__half>(p, parts, st)
+                                            : type_grad<__nv_bfloat16>(p, parts, st);
     if (rc != TR_OK || a.dweight == nullptr) return rc;
     // its start overlaps the end of the kernel that it waits for
     cudaLaunchConfig_t cfg{};
