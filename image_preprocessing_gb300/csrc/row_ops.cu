@@ -96,10 +96,12 @@ template <int V> __host__ __device__ constexpr int shift_pitch(int cols) { retur
 template <int V>
 __device__ __forceinline__ void share_weight(const float* w, float* shared, int n) {
     const int pitch = shift_pitch<V>(n);
-    for (int i = threadIdx.x; i < V * pitch; i += blockDim.x) {
-        const int c = (i % pitch - 1) * V + i / pitch;
-        shared[i] = c >= 0 && c < n ? (w != nullptr ? w[c] : 1.0f) : 0.0f;
-    }
+    for (int k = threadIdx.x; k < pitch; k += blockDim.x)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (k - 1) * V + v;
+            shared[v * pitch + k] = c >= 0 && c < n ? (w != nullptr ? w[c] : 1.0f) : 0.0f;
+        }
 }
 
 // Weights of the pack that starts at column c = pack * V - s, s < V.  (Packs past the row's end read the last
