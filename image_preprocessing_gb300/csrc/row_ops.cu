@@ -184,7 +184,7 @@ template <int T> constexpr int kThreads = T == 32 ? 256 : T;
 
 // T threads take a row, thread i the packs i, i + T, ... (NV of them).
 template <typename E, RowWhat WHAT, int V, int T, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kThreads<T>, T == 32 && WHAT == kNormQ8 ? 3 : 1) row_kernel(const RowParams p) {
     extern __shared__ float shared_weight[];   // with SHIFT
     const int t = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
     const long long row = T == 32 ? (long long)blockIdx.x * (kThreads<T> / 32) + (threadIdx.x >> 5) : blockIdx.x;
@@ -212,24 +212,6 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) h[i][j] = add ? to_f(px[i].e[j]) + to_f(pr[i].e[j]) : to_f(px[i].e[j]);
-    float sum = 0.0f;
-    unsigned top = 0;   // |.| as bits: orders like the values, infinities and NaN on top
-    float w[V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if (WHAT != kQuantize) sum = fmaf(h[i][j], h[i][j], sum);
-            if (WHAT != kNorm) {
-                const float v = WHAT == kNormQ8 ? h[i][j] * w[j] : h[i][j];
-                top = max(top, __float_as_uint(v) & 0x7fffffffu);
-            }
-        }
-    }
-    float ftop = __uint_as_float(top);
-    reduce_row<T, true>(sum, ftop);
-    const float s = WHAT == kQuantize ? 1.0f : rsqrtf(sum / (float)n + p.eps);
     if (p.residual_out != nullptr) {
         E* ho = static_cast<E*>(p.residual_out) + row * p.residual_out_stride;
 #pragma unroll
@@ -240,6 +222,22 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
             store_pack<E, V>(ho, i * T * V + c0, n, o);
         }
     }
+    float sum = 0.0f;
+    unsigned top = 0;   // |.| as bits: orders like the values, infinities and NaN on top
+    float w[V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (WHAT != kQuantize) sum = fmaf(h[i][j], h[i][j], sum);
+            if (WHAT == kNormQ8) h[i][j] *= w[j];   // 8 bits are made of h w
+            if (WHAT != kNorm) top = max(top, __float_as_uint(h[i][j]) & 0x7fffffffu);
+        }
+    }
+    float ftop = __uint_as_float(top);
+    reduce_row<T, true>(sum, ftop);
+    const float s = WHAT == kQuantize ? 1.0f : rsqrtf(sum / (float)n + p.eps);
     if constexpr (WHAT == kNorm) {
         E* out = static_cast<E*>(p.out) + row * p.out_stride;
 #pragma unroll
@@ -259,12 +257,11 @@ __global__ void __launch_bounds__(kThreads<T>) row_kernel(const RowParams p) {
         const uint32_t keep = finite ? 0xffffffffu : 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
             Pack<int8_t, V> o;
             uint32_t b[V];
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                b[j] = round_bits(__fmul_rn(WHAT == kNormQ8 ? h[i][j] * s * w[j] : h[i][j], k)) & keep;
+                b[j] = round_bits(__fmul_rn(WHAT == kNormQ8 ? h[i][j] * s : h[i][j], k)) & keep;
             if constexpr (V >= 4) {
                 uint32_t* words = reinterpret_cast<uint32_t*>(&o.word);
 #pragma unroll
