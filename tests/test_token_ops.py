@@ -356,7 +356,7 @@ def test_int8_matmul_tokens(M, dtype):
 @gpu
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 5000, 2048), (48, 1000, 8192), (300, 384, 20000), (1024, 1024, 768),
                                    (2049, 515, 640), (4000, 1536, 1023), (12544, 256, 128), (2049, 1539, 640), (1100, 4097, 333), (515, 4096, 1040), (20000, 1000, 65),
-                                   (8192, 300, 2100), (700, 9000, 4096)])
+                                   (8192, 300, 2100), (700, 9000, 4096), (30001, 1000, 200), (21000, 2050, 130)])
 def test_int8_matmul_larger(M, N, K):
     g = torch.Generator(device="cuda").manual_seed(M + N + K)
     check_product(any_int8(g, M, K), any_int8(g, N, K), torch.float32, True)
