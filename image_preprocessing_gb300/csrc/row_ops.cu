@@ -54,7 +54,7 @@ union Pack {
 // Values c .. c+V-1 of a row of n, zeros outside 0 .. n-1.  V > 1 only where
 // the row's value c lies on a boundary of the access.  `over`: the bytes next to
 // the row, up to the boundary, belong to the matrix too and may be read (they
-// are not used).
+// are not used, so it does not matter whether another CTA writes them meanwhile).
 template <typename E, int V>
 __device__ __forceinline__ Pack<E, V> load_pack(const E* row, int c, int n, bool over) {
     Pack<E, V> p;
@@ -542,22 +542,32 @@ __global__ void __launch_bounds__(kThreads<T>) grad_kernel(const GradParams p) {
     }
 }
 
-// dweight = sum of the partial rows: 32 columns to a CTA, 32 rows of threads,
-// each summing every 32nd partial in order, then the 32 sums in order.
-__global__ void __launch_bounds__(1024) grad_sum_kernel(const float* partial, float* dweight, int parts, int cols) {
-    __shared__ float sm[32][33];
+// dweight = sum of the partial rows: 8 columns (a sector of a row) to a CTA,
+// 128 threads each summing every 128th partial in order, then the 128 sums in
+// order, 16 at a time.
+constexpr int kSumCols = 8, kSumRows = 128;
+__global__ void __launch_bounds__(kSumCols * kSumRows) grad_sum_kernel(const float* partial, float* dweight, int parts, int cols) {
+    __shared__ float sm[kSumRows][kSumCols + 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are the kernel's before
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + x;
     float v = 0.0f;
     if (c < cols) {
-#pragma unroll 5
-        for (int r = threadIdx.y; r < parts; r += 32) v += partial[(long long)r * cols + c];
+#pragma unroll 8
+        for (int r = y; r < parts; r += kSumRows) v += partial[(long long)r * cols + c];
     }
-    sm[threadIdx.y][threadIdx.x] = v;
+    sm[y][x] = v;
     __syncthreads();
-    if (threadIdx.y == 0 && c < cols) {
+    if (y < kSumRows / 16) {
+        v = sm[y * 16][x];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) v += sm[i][threadIdx.x];
+        for (int i = 1; i < 16; ++i) v += sm[y * 16 + i][x];
+    }
+    __syncthreads();
+    if (y < kSumRows / 16) sm[y][x] = v;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < kSumRows / 16; ++i) v += sm[i][x];
         dweight[c] = v;
     }
 }
@@ -701,8 +711,8 @@ int launch_row_grad(const RowGradArgs& a) {
     if (rc != TR_OK || a.dweight == nullptr) return rc;
     // its start overlaps the end of the kernel that it waits for
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.cols + 31) / 32));
-    cfg.blockDim = dim3(32, 32);
+    cfg.gridDim = dim3((unsigned)((a.cols + kSumCols - 1) / kSumCols));
+    cfg.blockDim = dim3(kSumCols * kSumRows);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

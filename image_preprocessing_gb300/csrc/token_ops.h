@@ -10,6 +10,8 @@
 
 namespace trfn {
 
+constexpr int kMaxDevices = 64;
+
 // Norm or quantisation of rows; what == kQuantize has no residual, weight or eps.
 enum RowWhat { kNorm, kNormQ8, kQuantize };
 struct RowArgs {

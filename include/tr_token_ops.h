@@ -25,7 +25,8 @@
  *     another buffer is TR_ERR_INVALID_ARGUMENT.  Matrices interleaved in one
  *     buffer (column blocks with the same row distance in bytes) do not
  *     overlap; with different row distances, ranges that cross are refused.
- *   - rows = 0 is no work (a dweight is still written: zeros).
+ *   - rows = 0 is no work (a dweight is still written: zeros); cols is at least 1.
+ *   - Calls that may run at the same time need workspaces of their own.
  */
 #ifndef TR_TOKEN_OPS_H
 #define TR_TOKEN_OPS_H
@@ -67,8 +68,9 @@ typedef enum tr_elem {
  *   residual_out receives h, rounded to dtype; or NULL.  Only with residual.
  *   scale        rows binary32, written for TR_ELEM_I8 (else ignored).
  * h is formed, squared, summed and scaled in binary32 and rounded once per
- * output: y is made from the unrounded h.  out and residual_out may be x or
- * residual (not both the same matrix).
+ * output: y is made from the unrounded h.  (A row whose squares sum beyond
+ * binary32, |h| from 2^59 or so, gives y = 0, as the formula does in binary32.)  out
+ * and residual_out may be x or residual (not both the same matrix).
  * Errors: TR_ERR_INVALID_ARGUMENT for bad pointers, strides, types, overlaps,
  * an eps that is negative or not finite; TR_ERR_NOT_SUPPORTED for
  * cols > TR_MAX_ROW or rows > 2^31 - 1.                                     */
