@@ -182,9 +182,13 @@ struct RowParams {
 // Rows of T = 32 threads share a CTA of 256; longer rows have a CTA each.
 template <int T> constexpr int kThreads = T == 32 ? 256 : T;
 
+// CTAs of one-warp rows that an SM is to hold: enough rows under way, without spills.
+template <int V, int T, RowWhat WHAT>
+constexpr int kResident = T > 32 || V == 1 ? 1 : WHAT == kNormQ8 ? 3 : WHAT == kQuantize ? (V == 8 ? 5 : 4) : (V == 8 ? 4 : 2);
+
 // T threads take a row, thread i the packs i, i + T, ... (NV of them).
 template <typename E, RowWhat WHAT, int V, int T, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kThreads<T>, T == 32 && WHAT == kNormQ8 ? 3 : 1) row_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel(const RowParams p) {
     extern __shared__ float shared_weight[];   // with SHIFT
     const int t = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
     const long long row = T == 32 ? (long long)blockIdx.x * (kThreads<T> / 32) + (threadIdx.x >> 5) : blockIdx.x;
