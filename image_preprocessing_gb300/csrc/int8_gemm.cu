@@ -16,9 +16,10 @@
 //
 // Measured: 12544 x 4096 x 4096 240 us, 1755 TFLOP/s, of which the copies take
 // 35 us at 5.8 TB/s and the product runs at 1930 TFLOP/s, the rate of a plain
-// binary16 product; 50176 x 1024 x 768 68 us, 21 of them copies.  Converting in
-// the product's kernel instead would double what goes through shared memory for
-// each block, which the product already reads at two thirds of its rate.
+// binary16 product; 50176 x 1024 x 768 68.7 us, 21 of them copies; 50176 x 4096 x
+// 1024 231 us, 1825 TFLOP/s.  Converting in the product's kernel instead would
+// put half as much again through shared memory for each block; copying later
+// tokens beside the product of the first measured slower (73 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -17,6 +17,14 @@
 // (the usual case: equal strides, aligned buffers): then row r starts
 // s = r * stride mod V values into a pack, and lane i's pack holds columns
 // i V - s ... (SHIFT).  Any other alignment goes value by value.
+//
+// Measured (of the 6.68 TB/s copy rate): norm with residual 50176 x 1024
+// binary16 61.3 us (1.00), 12544 x 4096 bfloat16 61.6 us (1.00) and with 8-bit
+// output 54.8 us (0.98); quantisation 50176 x 768 20.9 us (0.83), reading back
+// 18.7 us (0.93); gradients 50176 x 1024 77.6 us (0.79), 12544 x 4096 76 us
+// (0.81), where the instructions, 22 a value with the weights' sums, take half of
+// the issue slots.  With shifted packs the ends of rows cost instructions: norm
+// 50176 x 999 80.7 us (0.74).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -385,9 +393,8 @@ __device__ __forceinline__ Two mul_two(Two a, Two b) {
 // in every row, so it keeps their weights and their sums of dweight in
 // registers, and the CTA writes the sums as one partial row.  (With SHIFT the
 // columns depend on the row's place in a pack; the grid and the rows of a CTA
-// are multiples of 8, so that this stays the same too.)  With 16 columns to a
-// thread the arithmetic, about 10 instructions a value, is what competes with
-// HBM: it works on pairs of binary32.
+// are multiples of 8, so that this stays the same too.)  The arithmetic
+// competes with HBM: it works on pairs of binary32.
 //
 // A thread copies its packs of the next rows into shared memory while it works
 // on this one; they are its own, so no barrier is needed.  kAhead rows ahead:

@@ -9,6 +9,9 @@
  * augmentation into one memory traversal" (tech-renaissance.cn/blog/?p=487)
  * describes as CPU SIMD code; here it runs as hand-written CUDA for sm_103a.
  *
+ * What follows the batch (norms of hidden rows, 8-bit rows, the integer matrix
+ * product) is declared in tr_token_ops.h.
+ *
  * Conventions for every entry point:
  *   - Return a tr_status code; nothing throws across this boundary.
  *   - Arguments are checked on the host before anything is launched; a call
