@@ -600,3 +600,31 @@ def test_python_refusals_on_the_gpu():
                  lambda: trfn.tr_int8_matmul(q, v[:3], q, v[:4], m[:, :4])):
         with pytest.raises(TrError):
             call()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=name_of)
+@pytest.mark.parametrize("cols", [3, 257, 999, 1021, 2049, 8191])
+def test_odd_rows_in_place_and_repeated(cols, dtype):
+    """Rows off 16-byte boundaries whose ends share 16 bytes with their
+    neighbours: outputs over inputs, a repeated row, no weights."""
+    b = Buffers(cols + 7)
+    rows = 37
+    base, row = b.randn(rows, cols).to(dtype), b.randn(1, cols).to(dtype)
+    w = 1 + 0.2 * b.randn(cols)
+    h, y = norm_exact(base, row.expand(rows, cols), w, 1e-5)
+    x, r = base.clone(), row.expand(rows, cols).contiguous()
+    trfn.tr_rms_norm(x, x, weight=w, residual=r, residual_out=r, eps=1e-5)
+    near(r, h, 2.0 ** -24 * h.abs(), dtype)
+    near(x, y, ROW * y.abs(), dtype)
+    x, out = base.clone(), torch.empty_like(base)
+    trfn.tr_rms_norm(x, out, weight=w, residual=row.expand(rows, cols), residual_out=x, eps=1e-5)   # stride 0
+    near(x, h, 2.0 ** -24 * h.abs(), dtype)
+    near(out, y, ROW * y.abs(), dtype)
+    q, scale = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    trfn.tr_rms_norm(base, q, scale=scale, eps=1e-5)
+    check_q8(q, scale, norm_exact(base, None, None, 1e-5)[1], ROW)
+    dy, stored = b.randn(rows, cols).to(dtype), base.clone()
+    want, size, _, _ = grad_exact(dy, stored, None, None, 1e-6)
+    trfn.tr_rms_norm_backward(dy, stored, stored)   # over h
+    near(stored, want, 2.0 ** -17 * size, dtype)
