@@ -114,9 +114,10 @@ __device__ __forceinline__ void share_weight(const float* w, float* shared, int 
 
 // Weights of the pack that starts at column c = pack * V - s, s < V.  (Packs past the row's end read the last
 // place: their values are not used.)
-template <int V, bool SHIFT>
+// SHARED: from shared memory; else, for rows that have a CTA each, one value at a time.
+template <int V, bool SHIFT, bool SHARED>
 __device__ __forceinline__ void load_weight(const float* w, const float* shared, int c, int pack, int s, int n, float (&v)[V]) {
-    if constexpr (SHIFT) {
+    if constexpr (SHIFT && SHARED) {
         const int place = min(pack, shift_pitch<V>(n) - 2);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = shared[((j - s) & (V - 1)) * shift_pitch<V>(n) + (j < s ? 0 : 1) + place];
@@ -127,7 +128,7 @@ __device__ __forceinline__ void load_weight(const float* w, const float* shared,
         for (int j = 0; j < V; ++j) v[j] = 1.0f;
         return;
     }
-    if constexpr (V >= 4) {
+    if constexpr (V >= 4 && !SHIFT) {
         if (c + V <= n) {
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
@@ -138,7 +139,7 @@ __device__ __forceinline__ void load_weight(const float* w, const float* shared,
         }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = (c + j < n) ? w[c + j] : 0.0f;
+    for (int j = 0; j < V; ++j) v[j] = (c + j >= 0 && c + j < n) ? w[c + j] : 0.0f;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -151,7 +152,16 @@ __device__ __forceinline__ float warp_sum(float v) {
 // over the T threads of a row, in a fixed order.
 template <int T, bool Q>
 __device__ __forceinline__ void reduce_row(float& a, float& b) {
-    __shared__ float sa[T / 32], sb[T / 32];
+    if constexpr (T < 32) {
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            const float c = __shfl_xor_sync(0xffffffffu, b, o);
+            b = Q ? __uint_as_float(max(__float_as_uint(b), __float_as_uint(c))) : b + c;
+        }
+        return;
+    }
+    __shared__ float sa[T < 32 ? 1 : T / 32], sb[T < 32 ? 1 : T / 32];
     a = warp_sum(a);
     if (Q) b = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b)));
     else b = warp_sum(b);
@@ -187,8 +197,8 @@ struct RowParams {
     float eps;
 };
 
-// Rows of T = 32 threads share a CTA of 256; longer rows have a CTA each.
-template <int T> constexpr int kThreads = T == 32 ? 256 : T;
+// Rows of T = 8 or 32 threads share a CTA of 256; longer rows have a CTA each.
+template <int T> constexpr int kThreads = T <= 32 ? 256 : T;
 
 // CTAs of one-warp rows that an SM is to hold: enough rows under way, without spills.
 template <int V, int T, RowWhat WHAT>
@@ -198,10 +208,10 @@ constexpr int kResident = T > 32 || V == 1 ? 1 : WHAT == kNormQ8 ? 3 : WHAT == k
 template <typename E, RowWhat WHAT, int V, int T, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel(const RowParams p) {
     extern __shared__ float shared_weight[];   // with SHIFT
-    const int t = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
-    const long long row = T == 32 ? (long long)blockIdx.x * (kThreads<T> / 32) + (threadIdx.x >> 5) : blockIdx.x;
-    const bool some = T > 32 || row < p.rows;
-    if (!SHIFT && !some) return;
+    const int t = threadIdx.x % T;
+    const long long row = (long long)blockIdx.x * (kThreads<T> / T) + threadIdx.x / T;
+    const bool some = T > 32 || row < p.rows;   // (threads of no row stay for the barrier, or for their warp)
+    if (T == 32 && !SHIFT && !some) return;
     const int n = some ? p.cols : 0, shift = SHIFT ? (int)((row * p.x_stride) & (V - 1)) : 0, c0 = t * V - shift;
     const E* x = static_cast<const E*>(p.x) + row * p.x_stride;
     Pack<E, V> px[NV], pr[NV];
@@ -214,11 +224,11 @@ __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel
         for (int i = 0; i < NV; ++i)
             pr[i] = load_pack<E, V>(r, i * T * V + c0, n, SHIFT && may_over(row, p.rows, p.residual_stride, V));
     }
-    if constexpr (SHIFT && WHAT != kQuantize) {   // while the rows are on their way
+    if constexpr (SHIFT && T <= 32 && WHAT != kQuantize) {   // while the rows are on their way
         share_weight<V>(p.weight, shared_weight, p.cols);
         __syncthreads();
     }
-    if (!some) return;
+    if (T == 32 && !some) return;
     float h[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel
     float w[V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (WHAT == kNormQ8) load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
+        if (WHAT == kNormQ8) load_weight<V, SHIFT, T <= 32>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (WHAT != kQuantize) sum = fmaf(h[i][j], h[i][j], sum);
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel
         E* out = static_cast<E*>(p.out) + row * p.out_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            load_weight<V, SHIFT>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
+            load_weight<V, SHIFT, T <= 32>(p.weight, shared_weight, i * T * V + c0, i * T + t, shift, n, w);
             Pack<E, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) o.e[j] = from_f<E>(h[i][j] * s * w[j]);
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel
         const float a = __float_as_uint(ftop) >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : s * ftop;
         const bool finite = fabsf(a) < __uint_as_float(0x7f800000u);
         const float k = finite && a >= kTiny ? 127.0f / a : 0.0f;
-        if (t == 0) p.scale[row] = !finite ? __uint_as_float(0x7fffffffu) : a >= kTiny ? a / 127.0f : 0.0f;
+        if (t == 0 && some) p.scale[row] = !finite ? __uint_as_float(0x7fffffffu) : a >= kTiny ? a / 127.0f : 0.0f;
         int8_t* out = static_cast<int8_t*>(p.out) + row * p.out_stride;
         const uint32_t keep = finite ? 0xffffffffu : 0u;
 #pragma unroll
@@ -292,14 +302,16 @@ template <typename E, RowWhat WHAT, int V, int T, int EPT, bool SHIFT>
 void start_rows(const RowParams& p, cudaStream_t st) {
     const long long per = kThreads<T> / T;
     row_kernel<E, WHAT, V, T, EPT / V, SHIFT>
-        <<<(unsigned)((p.rows + per - 1) / per), kThreads<T>, SHIFT && WHAT != kQuantize ? V * shift_pitch<V>(p.cols) * sizeof(float) : 0, st>>>(p);
+        <<<(unsigned)((p.rows + per - 1) / per), kThreads<T>, SHIFT && T <= 32 && WHAT != kQuantize ? V * shift_pitch<V>(p.cols) * sizeof(float) : 0, st>>>(p);
 }
 
 // Threads for a row, and values for a thread, by the row's length alone.
 template <typename E, RowWhat WHAT, int V, bool SHIFT>
 void pick_rows(const RowParams& p, cudaStream_t st) {
     const int n = p.cols + (SHIFT ? V - 1 : 0);
-    if (n <= 256) start_rows<E, WHAT, V, 32, 8, SHIFT>(p, st);
+    if (n <= 64) start_rows<E, WHAT, V, 8, 8, SHIFT>(p, st);
+    else if (n <= 128) start_rows<E, WHAT, V, 8, 16, SHIFT>(p, st);
+    else if (n <= 256) start_rows<E, WHAT, V, 32, 8, SHIFT>(p, st);
     else if (n <= 512) start_rows<E, WHAT, V, 32, 16, SHIFT>(p, st);
     else if (n <= 768) start_rows<E, WHAT, V, 32, 24, SHIFT>(p, st);
     else if (n <= 1024) start_rows<E, WHAT, V, 32, 32, SHIFT>(p, st);
@@ -666,9 +678,71 @@ __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, const flo
     }
 }
 
+// Rows of equal distance in q and out as one line, in packs of V values whose
+// places are on boundaries of the access whatever the rows' length; a pack may
+// hold the end of one row and the start of the next.  Four packs to a thread.
+template <typename E, int V, typename Index>
+__global__ void __launch_bounds__(256) dequant_line_kernel(const int8_t* q, const float* scale, E* out, Index packs,
+                                                           Index length, Index stride, int cols) {
+    Pack<int8_t, V> in[4];
+    Index at[4], row[4];
+    int c[4];
+    bool one[4], two_rows[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const Index i = ((Index)blockIdx.x * 4 + u) * 256 + threadIdx.x;
+        at[u] = i * V;
+        row[u] = i < packs ? at[u] / stride : 0;
+        c[u] = (int)(at[u] - row[u] * stride < (Index)cols ? at[u] - row[u] * stride : cols);   // past the row: none
+        one[u] = i < packs && c[u] + V <= cols;
+        // the rest of a row and the start of the next, without a gap
+        two_rows[u] = i < packs && !one[u] && stride == (Index)cols && cols >= V && at[u] + V <= length;
+        if (one[u] || two_rows[u]) in[u].word = *reinterpret_cast<const typename Word<V>::T*>(q + at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (one[u] || two_rows[u]) {
+            const float s0 = scale[row[u]], s1 = two_rows[u] ? scale[row[u] + 1] : s0;
+            Pack<E, V> o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const uint32_t b = (uint32_t)(uint8_t)in[u].e[j] ^ 0x80u;
+                o.e[j] = from_f<E>((__uint_as_float(0x4B000000u | b) - 8388736.0f) * (c[u] + j < cols ? s0 : s1));
+            }
+            *reinterpret_cast<typename Word<sizeof(E) * V>::T*>(out + at[u]) = o.word;
+        } else if (at[u] < length) {
+            for (int j = 0; j < V && at[u] + j < length; ++j) {
+                const Index f = at[u] + j, r = f / stride;
+                if (f - r * stride < (Index)cols) out[f] = from_f<E>((float)q[f] * scale[r]);
+            }
+        }
+    }
+}
+
+template <typename E, typename Index>
+int start_line(const DequantArgs& a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(E);
+    const Index length = (Index)(a.rows - 1) * (Index)a.q_stride + (Index)a.cols, packs = (length + V - 1) / V;
+    const Index ctas = (packs + 1023) / 1024;
+    if (ctas > 0x7fffffffu) return TR_ERR_NOT_SUPPORTED;
+    dequant_line_kernel<E, V, Index><<<(unsigned)ctas, 256, 0, st>>>(a.q, a.scale, static_cast<E*>(a.out), packs, length,
+                                                                     (Index)a.q_stride, a.cols);
+    return launched("dequantisation kernel");
+}
+
 template <typename E>
 int type_dequant(const DequantArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(E);
+    // Short rows, and rows without gaps off the boundaries, as one line (41241 x 69 binary16: 19.6 us by
+    // spans, 3.6 as a line; 20000 x 1001: 19.1 and 12.8; with gaps, 37248 x 176 in rows of 192, 7.0 and 11.2;
+    // aligned rows without, 50176 x 768, 18.8 and 22.3).
+    const bool starts = (uintptr_t)a.q % V == 0 && (uintptr_t)a.out % 16 == 0, line = a.q_stride == a.out_stride && starts;
+    const bool dense = a.q_stride == a.cols;
+    if (line && ((dense && (a.cols < 512 || a.cols % V != 0)) || (a.cols < 128 && a.q_stride <= 2 * (long long)a.cols))) {
+        const double length = (double)a.rows * (double)a.q_stride;
+        if (length < 4.0e9) return start_line<E, unsigned>(a, st);
+        if (length < 1.0e12) return start_line<E, unsigned long long>(a, st);
+    }
     const bool wide = on_pack(a.q, a.q_stride, 1, V, a.rows) && on_pack(a.out, a.out_stride, sizeof(E), V, a.rows);
     const long long spans_a_row = (a.cols + kSpan - 1) / kSpan;
     // rows beyond a grid's reach in further launches
