@@ -391,11 +391,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                             if (m0 + r < p.M) *reinterpret_cast<uint4*>(y + r * p.y_stride + part_q * V) = w;
                         }
                     } else {
-                        constexpr int R = 32 / C;   // rows of C values at a time
-                        for (int r = lane / C; r < 32; r += R) {
-                            const int e = lane % C, part_q = e / V;
-                            const E w = *(reinterpret_cast<const E*>(pass + r * 64 + ((part_q ^ (r >> 1)) & 3) * 16) + e % V);
-                            if (m0 + r < p.M && n + e < p.N) y[r * p.y_stride + e] = w;
+                        // rows off 16 bytes: R rows of C values at a time, eight reads before the writes
+                        constexpr int R = 32 / C;
+                        const int e = lane % C, part_q = e / V;
+                        const bool in = n + e < p.N;
+#pragma unroll
+                        for (int r0 = 0; r0 < 32; r0 += 8 * R) {
+                            E w[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const int r = r0 + u * R + lane / C;
+                                w[u] = *(reinterpret_cast<const E*>(pass + r * 64 + ((part_q ^ (r >> 1)) & 3) * 16) + e % V);
+                            }
+                            E* yr = y + (long long)(r0 + lane / C) * p.y_stride + e;
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                if (in && m0 + r0 + u * R + lane / C < p.M) *yr = w[u];
+                                yr += R * p.y_stride;
+                            }
                         }
                     }
                     __syncwarp();
