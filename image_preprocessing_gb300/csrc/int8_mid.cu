@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
         }
     };
     if (tid < CONVERT) {
+        // what the kernel before this one in the stream writes may be x or w, and what it reads y
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         // rows past the end repeat the last: their sums are not written
 #pragma unroll
         for (int j = 0; j < WP; ++j) wr[j] = p.w.p + (long long)min(n0 + row0 + kPass * j, p.w.rows - 1) * p.w.stride;
@@ -422,12 +424,15 @@ int start_mid(const MidParams& p, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads<T>);
     cfg.dynamicSmemBytes = kSmemBytes<T>;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)p.split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // barriers and TMEM are set up while the kernel before ends
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, mid_kernel<E, T, ONE, ON16>, p);
     if (e != cudaSuccess) {
         set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
