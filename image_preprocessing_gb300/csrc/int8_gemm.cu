@@ -118,7 +118,8 @@ struct CopyParams {
 // instructions, not the bytes, are the bound.)
 template <bool ON16>
 __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // x and w may be of the kernel before this one in the stream, which may read the workspace
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int q = threadIdx.x & 3, r = threadIdx.x >> 2;
     for (unsigned i = blockIdx.x; i < p.blocks; i += gridDim.x) {
         const bool of_w = i >= p.x_blocks;
@@ -298,6 +299,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             if (me < BN && n < p.N) v.channel = make_float2(p.w_scale[n], p.bias != nullptr ? p.bias[n] : 0.0f);
             return v;
         };
+        // the scales, and what reads y, may be of kernels before the copies, which have waited for them
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         Scales ahead = scales_of(pair);
         int half = 0, buf = 0;
         uint32_t half_phase = 0;
@@ -552,8 +555,20 @@ int launch_int8_gemm(const MatmulArgs& a) {
     c.xh = static_cast<uint4*>(a.workspace);
     c.wh = c.xh + x_blocks * (kBlockBytes / 16);
     const bool on16 = rows_on16(a.x, a.x_stride, a.M) && rows_on16(a.w, a.w_stride, a.N);
-    if (on16) copy_kernel<true><<<c.blocks, 256, 0, st>>>(c);
-    else copy_kernel<false><<<c.blocks, 256, 0, st>>>(c);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c.blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];   // its CTAs may be set up while the kernel before ends
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, on16 ? copy_kernel<true> : copy_kernel<false>, c);
+    if (e != cudaSuccess) {
+        set_last_error("cudaLaunchKernelEx(int8 copies)", (int)e);
+        return TR_ERR_CUDA;
+    }
     const int rc = launched("int8 copy kernel");
     if (rc != TR_OK) return rc;
     const Copies copies{c.xh, c.wh, x_blocks * kBlockRows, w_blocks * kBlockRows};

@@ -36,6 +36,7 @@ template <typename E, int M, int KP, bool ON16>
 __global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
     constexpr int NT = kWarps / KP * kRows;   // channels of a CTA
     __shared__ int sums[KP][M][NT];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the kernel before this one in the stream
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp % KP, group = warp / KP;
     const int n0 = blockIdx.x * NT;
@@ -107,25 +108,36 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
 }
 
 template <typename E, int M, int KP>
-void start_few(const FewParams& p, bool on16, cudaStream_t st) {
+int start_few(const FewParams& p, bool on16, cudaStream_t st) {
     constexpr int NT = kWarps / KP * kRows;
-    const unsigned grid = (unsigned)((p.w.rows + NT - 1) / NT);
-    if (on16) few_kernel<E, M, KP, true><<<grid, kWarps * 32, 0, st>>>(p);
-    else few_kernel<E, M, KP, false><<<grid, kWarps * 32, 0, st>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.w.rows + NT - 1) / NT));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];   // its CTAs may be set up while the kernel before ends
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, on16 ? few_kernel<E, M, KP, true> : few_kernel<E, M, KP, false>, p);
+    if (e != cudaSuccess) {
+        set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
+        return TR_ERR_CUDA;
+    }
+    return launched("int8 product kernel (few tokens)");
 }
 
 template <typename E, int M>
-void part_few(const FewParams& p, bool on16, cudaStream_t st) {
+int part_few(const FewParams& p, bool on16, cudaStream_t st) {
     // K in 8 parts where the channels alone do not give each SM four CTAs of two
     // (1 x 4096 x 16384: 15.1 us in 2 parts, 14.8 in 8; 1 x 16384 x 4096: 14.9 and 17.7)
-    if (p.w.rows >= 152 * kWarps * kRows / 2) start_few<E, M, 2>(p, on16, st);
-    else start_few<E, M, 8>(p, on16, st);
+    if (p.w.rows >= 152 * kWarps * kRows / 2) return start_few<E, M, 2>(p, on16, st);
+    return start_few<E, M, 8>(p, on16, st);
 }
 
 template <typename E>
-void pick_few(const FewParams& p, bool on16, cudaStream_t st) {
-    if (p.x.rows == 1) part_few<E, 1>(p, on16, st);
-    else part_few<E, 2>(p, on16, st);
+int pick_few(const FewParams& p, bool on16, cudaStream_t st) {
+    return p.x.rows == 1 ? part_few<E, 1>(p, on16, st) : part_few<E, 2>(p, on16, st);
 }
 
 int launch_few(const MatmulArgs& a) {
@@ -139,10 +151,9 @@ int launch_few(const MatmulArgs& a) {
     p.y_stride = a.y_stride;
     const bool on16 = rows_on16(a.x, a.x_stride, a.M) && rows_on16(a.w, a.w_stride, a.N);
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-    if (a.out_dtype == TR_ELEM_F32) pick_few<float>(p, on16, st);
-    else if (a.out_dtype == TR_ELEM_F16) pick_few<__half>(p, on16, st);
-    else pick_few<__nv_bfloat16>(p, on16, st);
-    return launched("int8 product kernel (few tokens)");
+    if (a.out_dtype == TR_ELEM_F32) return pick_few<float>(p, on16, st);
+    if (a.out_dtype == TR_ELEM_F16) return pick_few<__half>(p, on16, st);
+    return pick_few<__nv_bfloat16>(p, on16, st);
 }
 
 // By shape alone, so that the workspace is known before the matrices are.

@@ -185,6 +185,31 @@ __device__ __forceinline__ void reduce_row(float& a, float& b) {
 // conversion instruction takes several times as long).
 __device__ __forceinline__ uint32_t round_bits(float v) { return __float_as_uint(__fadd_rn(v, 12582912.0f)); }
 
+// Every kernel here is launched so that its CTAs may be set up while the kernel before it in the stream ends,
+// and waits for that kernel before it touches memory.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_row_kernel(const char* what, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                      A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    if (e != cudaSuccess) {
+        set_last_error(what, (int)e);
+        return TR_ERR_CUDA;
+    }
+    return launched(what);
+}
+
 struct RowParams {
     const void* x;
     const void* residual;
@@ -208,6 +233,7 @@ constexpr int kResident = T > 32 || V == 1 ? 1 : WHAT == kNormQ8 ? 3 : WHAT == k
 template <typename E, RowWhat WHAT, int V, int T, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel(const RowParams p) {
     extern __shared__ float shared_weight[];   // with SHIFT
+    wait_for_previous();
     const int t = threadIdx.x % T;
     const long long row = (long long)blockIdx.x * (kThreads<T> / T) + threadIdx.x / T;
     const bool some = T > 32 || row < p.rows;   // (threads of no row stay for the barrier, or for their warp)
@@ -299,30 +325,32 @@ __global__ void __launch_bounds__(kThreads<T>, kResident<V, T, WHAT>) row_kernel
 
 
 template <typename E, RowWhat WHAT, int V, int T, int EPT, bool SHIFT>
-void start_rows(const RowParams& p, cudaStream_t st) {
+int start_rows(const RowParams& p, cudaStream_t st) {
     const long long per = kThreads<T> / T;
-    row_kernel<E, WHAT, V, T, EPT / V, SHIFT>
-        <<<(unsigned)((p.rows + per - 1) / per), kThreads<T>, SHIFT && T <= 32 && WHAT != kQuantize ? V * shift_pitch<V>(p.cols) * sizeof(float) : 0, st>>>(p);
+    const size_t smem = SHIFT && T <= 32 && WHAT != kQuantize ? V * shift_pitch<V>(p.cols) * sizeof(float) : 0;
+    return launch_row_kernel("row kernel", row_kernel<E, WHAT, V, T, EPT / V, SHIFT>, (unsigned)((p.rows + per - 1) / per),
+                             kThreads<T>, smem, st, p);
 }
 
 // Threads for a row, and values for a thread, by the row's length alone.
 template <typename E, RowWhat WHAT, int V, bool SHIFT>
-void pick_rows(const RowParams& p, cudaStream_t st) {
+int pick_rows(const RowParams& p, cudaStream_t st) {
     const int n = p.cols + (SHIFT ? V - 1 : 0);
-    if (n <= 64) start_rows<E, WHAT, V, 8, 8, SHIFT>(p, st);
-    else if (n <= 128) start_rows<E, WHAT, V, 8, 16, SHIFT>(p, st);
-    else if (n <= 256) start_rows<E, WHAT, V, 32, 8, SHIFT>(p, st);
-    else if (n <= 512) start_rows<E, WHAT, V, 32, 16, SHIFT>(p, st);
-    else if (n <= 768) start_rows<E, WHAT, V, 32, 24, SHIFT>(p, st);
-    else if (n <= 1024) start_rows<E, WHAT, V, 32, 32, SHIFT>(p, st);
-    else if (n <= 2048) start_rows<E, WHAT, V, 128, 16, SHIFT>(p, st);
-    else if (n <= 128 * 24) start_rows<E, WHAT, V, 128, 24, SHIFT>(p, st);
-    else if (n <= 4096) start_rows<E, WHAT, V, 128, 32, SHIFT>(p, st);
-    else if (SHIFT || n <= 8192) start_rows<E, WHAT, V, SHIFT ? 512 : 256, SHIFT ? 24 : 32, SHIFT>(p, st);
-    else if constexpr (!SHIFT) {
-        if (n <= 16384) start_rows<E, WHAT, V, 512, 32, SHIFT>(p, st);
-        else start_rows<E, WHAT, V, 1024, 32, SHIFT>(p, st);
+    if (n <= 64) return start_rows<E, WHAT, V, 8, 8, SHIFT>(p, st);
+    if (n <= 128) return start_rows<E, WHAT, V, 8, 16, SHIFT>(p, st);
+    if (n <= 256) return start_rows<E, WHAT, V, 32, 8, SHIFT>(p, st);
+    if (n <= 512) return start_rows<E, WHAT, V, 32, 16, SHIFT>(p, st);
+    if (n <= 768) return start_rows<E, WHAT, V, 32, 24, SHIFT>(p, st);
+    if (n <= 1024) return start_rows<E, WHAT, V, 32, 32, SHIFT>(p, st);
+    if (n <= 2048) return start_rows<E, WHAT, V, 128, 16, SHIFT>(p, st);
+    if (n <= 128 * 24) return start_rows<E, WHAT, V, 128, 24, SHIFT>(p, st);
+    if (n <= 4096) return start_rows<E, WHAT, V, 128, 32, SHIFT>(p, st);
+    if (SHIFT || n <= 8192) return start_rows<E, WHAT, V, SHIFT ? 512 : 256, SHIFT ? 24 : 32, SHIFT>(p, st);
+    if constexpr (!SHIFT) {
+        if (n <= 16384) return start_rows<E, WHAT, V, 512, 32, SHIFT>(p, st);
+        return start_rows<E, WHAT, V, 1024, 32, SHIFT>(p, st);
     }
+    return TR_ERR_NOT_SUPPORTED;   // not reached
 }
 
 // How the rows of a matrix lie on packs of V values of es bytes: 0 all of them
@@ -344,23 +372,23 @@ struct Phase {
 bool on_pack(const void* p, long long stride, int es, int V, long long rows) { return phase_of(p, stride, es, V, rows) == 0; }
 
 template <typename E, RowWhat WHAT>
-void align_rows(const RowParams& p, cudaStream_t st) {
+int align_rows(const RowParams& p, cudaStream_t st) {
     constexpr int es = sizeof(E), V = 16 / es;
     Phase phase;
     phase.add(p.x, p.x_stride, es, V, p.rows);
     phase.add(p.residual, p.residual_stride, es, V, p.rows);
     phase.add(p.out, p.out_stride, WHAT == kNorm ? es : 1, V, p.rows);
     phase.add(p.residual_out, p.residual_out_stride, es, V, p.rows);
-    if (phase.f == 0 && (uintptr_t)p.weight % 16 == 0) pick_rows<E, WHAT, V, false>(p, st);
-    else if (phase.f >= 0 && p.cols <= kShiftCols) pick_rows<E, WHAT, V, true>(p, st);
-    else pick_rows<E, WHAT, 1, false>(p, st);
+    if (phase.f == 0 && (uintptr_t)p.weight % 16 == 0) return pick_rows<E, WHAT, V, false>(p, st);
+    if (phase.f >= 0 && p.cols <= kShiftCols) return pick_rows<E, WHAT, V, true>(p, st);
+    return pick_rows<E, WHAT, 1, false>(p, st);
 }
 
 template <typename E>
-void type_rows(const RowParams& p, RowWhat what, cudaStream_t st) {
-    if (what == kNorm) align_rows<E, kNorm>(p, st);
-    else if (what == kNormQ8) align_rows<E, kNormQ8>(p, st);
-    else align_rows<E, kQuantize>(p, st);
+int type_rows(const RowParams& p, RowWhat what, cudaStream_t st) {
+    if (what == kNorm) return align_rows<E, kNorm>(p, st);
+    if (what == kNormQ8) return align_rows<E, kNormQ8>(p, st);
+    return align_rows<E, kQuantize>(p, st);
 }
 
 struct GradParams {
@@ -421,6 +449,7 @@ __global__ void __launch_bounds__(kThreads<T>) grad_kernel(const GradParams p) {
     static_assert(N % 2 == 0, "values are taken in pairs");
     constexpr int AHEAD = kAhead<V, T, NV>;
     extern __shared__ __align__(16) uint8_t dynamic[];
+    wait_for_previous();
     uint4* const mine = reinterpret_cast<uint4*>(dynamic) + threadIdx.x;   // AHEAD x 3 NV packs, kThreads<T> apart
     const int t = threadIdx.x % T, n = p.cols;
     const long long row0 = (long long)blockIdx.x * R + threadIdx.x / T, step = (long long)gridDim.x * R;
@@ -571,7 +600,7 @@ __global__ void __launch_bounds__(kThreads<T>) grad_kernel(const GradParams p) {
 constexpr int kSumCols = 8, kSumRows = 128;
 __global__ void __launch_bounds__(kSumCols * kSumRows) grad_sum_kernel(const float* partial, float* dweight, int parts, int cols) {
     __shared__ float sm[kSumRows][kSumCols + 1];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are the kernel's before
+    wait_for_previous();   // the partial rows are that kernel's
     const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + x;
     float v = 0.0f;
     if (c < cols) {
@@ -607,8 +636,7 @@ int start_grad(const GradParams& p, int parts, cudaStream_t st) {
             return TR_ERR_CUDA;
         }
     }
-    grad_kernel<E, V, T, NV, SHIFT><<<parts, kThreads<T>, smem, st>>>(p);
-    return launched("row gradient kernel");
+    return launch_row_kernel("row gradient kernel", grad_kernel<E, V, T, NV, SHIFT>, (unsigned)parts, kThreads<T>, smem, st, p);
 }
 
 template <typename E, int V, bool SHIFT>
@@ -645,6 +673,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, const flo
                                                       long long q_stride, long long out_stride, int cols,
                                                       unsigned spans_a_row) {
     constexpr int NV = V == 1 ? 4 : kSpan / (32 * V), LOOPS = kSpan / (32 * V * NV);
+    wait_for_previous();
     const unsigned span = blockIdx.x * 8u + (threadIdx.x >> 5);
     if (span >= spans) return;
     const unsigned row = span / spans_a_row;
@@ -684,6 +713,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, const flo
 template <typename E, int V, typename Index>
 __global__ void __launch_bounds__(256) dequant_line_kernel(const int8_t* q, const float* scale, E* out, Index packs,
                                                            Index length, Index stride, int cols) {
+    wait_for_previous();
     Pack<int8_t, V> in[4];
     Index at[4], row[4];
     int c[4];
@@ -725,9 +755,8 @@ int start_line(const DequantArgs& a, cudaStream_t st) {
     const Index length = (Index)(a.rows - 1) * (Index)a.q_stride + (Index)a.cols, packs = (length + V - 1) / V;
     const Index ctas = (packs + 1023) / 1024;
     if (ctas > 0x7fffffffu) return TR_ERR_NOT_SUPPORTED;
-    dequant_line_kernel<E, V, Index><<<(unsigned)ctas, 256, 0, st>>>(a.q, a.scale, static_cast<E*>(a.out), packs, length,
-                                                                     (Index)a.q_stride, a.cols);
-    return launched("dequantisation kernel");
+    return launch_row_kernel("dequantisation kernel", dequant_line_kernel<E, V, Index>, (unsigned)ctas, 256, 0, st, a.q, a.scale,
+                             static_cast<E*>(a.out), packs, length, (Index)a.q_stride, a.cols);
 }
 
 template <typename E>
@@ -751,13 +780,8 @@ int type_dequant(const DequantArgs& a, cudaStream_t st) {
         const unsigned spans = (unsigned)(rows * spans_a_row), grid = (spans + 7) / 8;
         const int8_t* q = a.q + r0 * a.q_stride;
         E* out = static_cast<E*>(a.out) + r0 * a.out_stride;
-        if (wide)
-            dequant_kernel<E, V><<<grid, 256, 0, st>>>(q, a.scale + r0, out, spans, a.q_stride, a.out_stride, a.cols,
-                                                       (unsigned)spans_a_row);
-        else
-            dequant_kernel<E, 1><<<grid, 256, 0, st>>>(q, a.scale + r0, out, spans, a.q_stride, a.out_stride, a.cols,
-                                                       (unsigned)spans_a_row);
-        const int rc = launched("dequantisation kernel");
+        const int rc = launch_row_kernel("dequantisation kernel", wide ? dequant_kernel<E, V> : dequant_kernel<E, 1>, grid, 256, 0,
+                                         st, q, a.scale + r0, out, spans, a.q_stride, a.out_stride, a.cols, (unsigned)spans_a_row);
         if (rc != TR_OK) return rc;
         r0 += rows;
     }
@@ -770,10 +794,9 @@ int launch_rows(const RowArgs& a) {
     RowParams p{a.x, a.residual, a.weight, a.out, a.residual_out, a.scale, a.rows, a.x_stride, a.residual_stride,
                 a.out_stride, a.residual_out_stride, a.cols, a.eps};
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-    if (a.dtype == TR_ELEM_F32) type_rows<float>(p, a.what, st);
-    else if (a.dtype == TR_ELEM_F16) type_rows<__half>(p, a.what, st);
-    else type_rows<__nv_bfloat16>(p, a.what, st);
-    return launched("row kernel");
+    if (a.dtype == TR_ELEM_F32) return type_rows<float>(p, a.what, st);
+    if (a.dtype == TR_ELEM_F16) return type_rows<__half>(p, a.what, st);
+    return type_rows<__nv_bfloat16>(p, a.what, st);
 }
 
 int row_grad_parts(long long rows, long long cols) {
@@ -794,22 +817,8 @@ int launch_row_grad(const RowGradArgs& a) {
                    : a.dtype == TR_ELEM_F16 ? type_grad<__half>(p, parts, st)
                                             : type_grad<__nv_bfloat16>(p, parts, st);
     if (rc != TR_OK || a.dweight == nullptr) return rc;
-    // its start overlaps the end of the kernel that it waits for
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.cols + kSumCols - 1) / kSumCols));
-    cfg.blockDim = dim3(kSumCols * kSumRows);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_sum_kernel, (const float*)a.partial, a.dweight, parts, a.cols);
-    if (e != cudaSuccess) {
-        set_last_error("cudaLaunchKernelEx(weight gradient sum)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    return launched("weight gradient sum kernel");
+    return launch_row_kernel("weight gradient sum kernel", grad_sum_kernel, (unsigned)((a.cols + kSumCols - 1) / kSumCols),
+                             kSumCols * kSumRows, 0, st, a.partial, a.dweight, parts, a.cols);
 }
 
 int launch_dequant(const DequantArgs& a) {
