@@ -14,10 +14,11 @@
 // products are read into integer registers while the other half of TMEM
 // takes the next 1024, so the reading is hidden.
 //
-// Measured: 12544 x 4096 x 4096 240 us, 1755 TFLOP/s, of which the copies take
+// Measured: 12544 x 4096 x 4096 240 to 249 us, 1690 to 1755 TFLOP/s, of which the copies take
 // 35 us at 5.8 TB/s and the product runs at 1930 TFLOP/s, the rate of a plain
 // binary16 product; 50176 x 1024 x 768 68.7 us, 21 of them copies; 50176 x 4096 x
-// 1024 231 us, 1825 TFLOP/s.  Converting in the product's kernel instead would
+// 1024 231 us, 1825 TFLOP/s; outputs off 16 bytes, 7168 x 8749 x 197, 54 us (93
+// with one row stored at a time).  Converting in the product's kernel instead would
 // put half as much again through shared memory for each block; copying later
 // tokens beside the product of the first measured slower (73 us).
 #include <cuda.h>
