@@ -51,3 +51,26 @@ def test_example_follows_the_network_in_binary32(images, width):
     exact = s * (1 - hd * s * s * hd.mean(1, keepdim=True))
     assert float((dx.double() - exact).norm() / exact.norm()) < 2.0 ** -8
     assert trfn.tr_device_status() == 0
+
+
+@pytest.mark.gpu
+def test_token_rows_after_overlapping_batches():
+    """Batches that overlap each other, then a token-row call on the output
+    before the last: it waits for all of them."""
+    mean, std, _ = trfn.tr_norm_preset("IMAGENET")
+    N, C = 64, 3
+    srcs = [torch.from_numpy(synth.pixels_uniform(20 + k, N, 224, 224, C)).cuda() for k in range(3)]
+    ws = [torch.zeros(trfn.tr_workspace_bytes(), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = torch.empty((N, 224, 224, C), dtype=torch.float16, device="cuda")
+    trfn.tr_fused_norm(srcs[1], want, mean, std, out_dtype=trfn.OUT_F16)
+    rows = want.view(N * 224, 224 * C)
+    q0, s0 = torch.empty(rows.shape, dtype=torch.int8, device="cuda"), torch.empty(rows.size(0), device="cuda")
+    trfn.tr_quantize_rows(rows, q0, s0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = [torch.zeros_like(want) for _ in range(3)]
+        q, s = torch.zeros_like(q0), torch.zeros_like(s0)
+        for k in range(3):
+            trfn.tr_fused_norm(srcs[k], outs[k], mean, std, out_dtype=trfn.OUT_F16, workspace=ws[k % 2], overlap_previous=True)
+        trfn.tr_quantize_rows(outs[1].view(N * 224, 224 * C), q, s)
+        assert torch.equal(q, q0) and torch.equal(s, s0)
