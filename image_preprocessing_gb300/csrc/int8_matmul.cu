@@ -156,8 +156,11 @@ int launch_few(const MatmulArgs& a) {
     return pick_few<__nv_bfloat16>(p, on16, st);
 }
 
-// By shape alone, so that the workspace is known before the matrices are.
-bool mid_takes(long long M, long long N, long long K) { return int8_mid_cycles(M, N, K) <= int8_gemm_cycles(M, N, K); }
+// By shape alone, so that the workspace is known before the matrices are.  A sum of nothing (K = 0) goes to the
+// kernel that takes no copies, whatever the size: there would be no blocks to copy.
+bool mid_takes(long long M, long long N, long long K) {
+    return K == 0 || int8_mid_cycles(M, N, K) <= int8_gemm_cycles(M, N, K);
+}
 
 }  // namespace
 

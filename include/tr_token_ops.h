@@ -121,7 +121,8 @@ size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K);
  *   workspace device, tr_int8_matmul_workspace_bytes() bytes, 16-byte aligned,
  *            not initialised; NULL where that is 0.
  * The sum is exact in integers; it is rounded to binary32 once, scaled, and
- * rounded to out_dtype.  K = 0 gives the bias.
+ * rounded to out_dtype.  K = 0 gives the bias (a sum of 0, which scales that
+ * are not finite make NaN).
  * TR_ERR_NOT_SUPPORTED for K > TR_MAX_INT8_K or M, N > TR_MAX_INT8_ROWS.    */
 int tr_int8_matmul(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
                    const float* bias, void* y, long long M, long long N, long long K, long long x_stride,

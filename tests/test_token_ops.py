@@ -628,3 +628,22 @@ def test_odd_rows_in_place_and_repeated(cols, dtype):
     want, size, _, _ = grad_exact(dy, stored, None, None, 1e-6)
     trfn.tr_rms_norm_backward(dy, stored, stored)   # over h
     near(stored, want, 2.0 ** -17 * size, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=name_of)
+@pytest.mark.parametrize("M,N", [(1, 4096), (2, 20000), (3, 7), (2048, 2048), (4096, 1024), (50176, 129)])
+def test_int8_matmul_of_nothing_gives_the_bias(M, N, dtype):
+    """K = 0 at every size, those among them that would take the copies of
+    many tokens."""
+    b = Buffers(M)
+    x, w = torch.empty(M, 0, dtype=torch.int8, device="cuda"), torch.empty(N, 0, dtype=torch.int8, device="cuda")
+    sx, sw, bias = b.randn(M), b.randn(N), b.randn(N)
+    assert trfn.tr_int8_matmul_workspace_bytes(M, N, 0) == 0
+    y = b.empty(M, N, dtype, 3, 1)
+    trfn.tr_int8_matmul(x, sx, w, sw, y, bias=bias)
+    assert torch.equal(y, bias.to(dtype).expand(M, N))
+    trfn.tr_int8_matmul(x, sx, w, sw, y)
+    assert y.count_nonzero().item() == 0
+    b.check_around()
+    assert trfn.tr_device_status() == 0
