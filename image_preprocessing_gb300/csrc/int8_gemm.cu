@@ -442,19 +442,13 @@ int block_map(CUtensorMap* map, void* p, long long rows, int box) {
             q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    if (encode == nullptr) {
-        set_last_error("cuTensorMapEncodeTiled unavailable", (int)cudaErrorNotSupported);
-        return TR_ERR_CUDA;
-    }
+    if (encode == nullptr) return cuda_failed("cuTensorMapEncodeTiled unavailable", (int)cudaErrorNotSupported);
     const cuuint64_t dims[2] = {kBlockK, (cuuint64_t)rows}, strides[1] = {kBlockK * 2};
     const cuuint32_t boxes[2] = {kBlockK, (cuuint32_t)box}, elem[2] = {1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, dims, strides, boxes, elem,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        set_last_error("cuTensorMapEncodeTiled", (int)cudaErrorInvalidValue);
-        return TR_ERR_CUDA;
-    }
+    if (r != CUDA_SUCCESS) return cuda_failed("cuTensorMapEncodeTiled", (int)cudaErrorInvalidValue);
     return TR_OK;
 }
 
@@ -482,20 +476,14 @@ int start_gemm(const GemmParams& q, const Copies& c, cudaStream_t st) {
     static std::atomic<int> known[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        set_last_error("cudaGetDevice", (int)e);
-        return TR_ERR_CUDA;
-    }
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_failed("cudaGetDevice", (int)e);
     std::atomic<int>& pairs = known[dev];
     int n = pairs.load(std::memory_order_relaxed);
     if (n == 0) {
         cfg.gridDim = dim3(2);
         e = cudaFuncSetAttribute(gemm_kernel<E, BN, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<BN>);
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel<E, BN, ONE>, &cfg);
-        if (e != cudaSuccess || n < 1) {
-            set_last_error("int8 product kernel set-up", (int)e);
-            return TR_ERR_CUDA;
-        }
+        if (e != cudaSuccess || n < 1) return cuda_failed("int8 product kernel set-up", (int)e);
         pairs.store(n, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)(2 * (tiles < n ? tiles : n)));
@@ -504,12 +492,7 @@ int start_gemm(const GemmParams& q, const Copies& c, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gemm_kernel<E, BN, ONE>, p);
-    if (e != cudaSuccess) {
-        set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    return launched("int8 product kernel");
+    return launched("int8 product kernel", (int)cudaLaunchKernelEx(&cfg, gemm_kernel<E, BN, ONE>, p));
 }
 
 template <typename E, int BN>
@@ -565,12 +548,7 @@ int launch_int8_gemm(const MatmulArgs& a) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, on16 ? copy_kernel<true> : copy_kernel<false>, c);
-    if (e != cudaSuccess) {
-        set_last_error("cudaLaunchKernelEx(int8 copies)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    const int rc = launched("int8 copy kernel");
+    const int rc = launched("int8 copy kernel", (int)cudaLaunchKernelEx(&cfg, on16 ? copy_kernel<true> : copy_kernel<false>, c));
     if (rc != TR_OK) return rc;
     const Copies copies{c.xh, c.wh, x_blocks * kBlockRows, w_blocks * kBlockRows};
     GemmParams p{};

@@ -119,12 +119,8 @@ int start_few(const FewParams& p, bool on16, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, on16 ? few_kernel<E, M, KP, true> : few_kernel<E, M, KP, false>, p);
-    if (e != cudaSuccess) {
-        set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    return launched("int8 product kernel (few tokens)");
+    return launched("int8 product kernel (few tokens)",
+                    (int)cudaLaunchKernelEx(&cfg, on16 ? few_kernel<E, M, KP, true> : few_kernel<E, M, KP, false>, p));
 }
 
 template <typename E, int M>

@@ -405,18 +405,12 @@ int start_mid(const MidParams& p, cudaStream_t st) {
     static std::atomic<bool> set_up[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        set_last_error("cudaGetDevice", (int)e);
-        return TR_ERR_CUDA;
-    }
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_failed("cudaGetDevice", (int)e);
     std::atomic<bool>& ready = set_up[dev];
     if (!ready.load(std::memory_order_relaxed)) {
         e = cudaFuncSetAttribute(mid_kernel<E, T, ONE, ON16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    kSmemBytes<T>);
-        if (e != cudaSuccess) {
-            set_last_error("int8 product kernel set-up", (int)e);
-            return TR_ERR_CUDA;
-        }
+        if (e != cudaSuccess) return cuda_failed("int8 product kernel set-up", (int)e);
         ready.store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg{};
@@ -433,12 +427,7 @@ int start_mid(const MidParams& p, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, mid_kernel<E, T, ONE, ON16>, p);
-    if (e != cudaSuccess) {
-        set_last_error("cudaLaunchKernelEx(int8 product)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    return launched("int8 product kernel");
+    return launched("int8 product kernel", (int)cudaLaunchKernelEx(&cfg, mid_kernel<E, T, ONE, ON16>, p));
 }
 
 template <typename E, int T>

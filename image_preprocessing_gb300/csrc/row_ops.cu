@@ -202,12 +202,7 @@ int launch_row_kernel(const char* what, void (*kernel)(P...), unsigned grid, uns
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-    if (e != cudaSuccess) {
-        set_last_error(what, (int)e);
-        return TR_ERR_CUDA;
-    }
-    return launched(what);
+    return launched(what, (int)cudaLaunchKernelEx(&cfg, kernel, P(args)...));
 }
 
 struct RowParams {
@@ -631,10 +626,7 @@ int start_grad(const GradParams& p, int parts, cudaStream_t st) {
     if (smem > 40 * 1024) {   // with the static part, beyond what needs no opt-in
         const cudaError_t e = cudaFuncSetAttribute(grad_kernel<E, V, T, NV, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)smem);
-        if (e != cudaSuccess) {
-            set_last_error("row gradient kernel set-up", (int)e);
-            return TR_ERR_CUDA;
-        }
+        if (e != cudaSuccess) return cuda_failed("row gradient kernel set-up", (int)e);
     }
     return launch_row_kernel("row gradient kernel", grad_kernel<E, V, T, NV, SHIFT>, (unsigned)parts, kThreads<T>, smem, st, p);
 }

@@ -9,12 +9,14 @@
 
 namespace trfn {
 
-int launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) {
-        set_last_error(what, (int)e);
-        return TR_ERR_CUDA;
-    }
+int cuda_failed(const char* what, int cuda_error) {
+    set_last_error(what, cuda_error);
+    (void)cudaGetLastError();
+    return TR_ERR_CUDA;
+}
+
+int launched(const char* what, int cuda_error) {
+    if (cuda_error != (int)cudaSuccess) return cuda_failed(what, cuda_error);
     count_launch();
     return TR_OK;
 }
@@ -150,9 +152,7 @@ int tr_rms_norm_backward(const void* dy, const void* h, const float* weight, con
     if (rows == 0) {
         if (dweight == nullptr) return TR_OK;
         const cudaError_t e = cudaMemsetAsync(dweight, 0, (size_t)cols * 4, static_cast<cudaStream_t>(stream));
-        if (e == cudaSuccess) return TR_OK;
-        set_last_error("cudaMemsetAsync(dweight)", (int)e);
-        return TR_ERR_CUDA;
+        return e == cudaSuccess ? TR_OK : cuda_failed("cudaMemsetAsync(dweight)", (int)e);
     }
     if (bad_input(my) || bad_input(mh) || bad_output(mx)) return TR_ERR_INVALID_ARGUMENT;
     if (dresidual != nullptr && bad_input(mr)) return TR_ERR_INVALID_ARGUMENT;

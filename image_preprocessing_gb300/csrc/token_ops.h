@@ -86,7 +86,11 @@ double int8_mid_cycles(long long M, long long N, long long K);
 int read_gemm_status(int* flags, bool clear);
 int read_mid_status(int* flags, bool clear);
 
-// cudaGetLastError() after a launch as a tr_status; counts the launch.
-int launched(const char* what);
+// A failed runtime call as a tr_status: keeps its text for tr_last_error_message, and takes it from the runtime's
+// last error, where another call would find it.
+int cuda_failed(const char* what, int cuda_error);
+// What a launch returned as a tr_status; counts the launch.  (Not cudaGetLastError(): an error that an earlier
+// call left would be reported for a kernel that runs, and a caller who repeats an in-place call does it twice.)
+int launched(const char* what, int cuda_error);
 
 }  // namespace trfn

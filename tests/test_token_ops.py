@@ -647,3 +647,32 @@ def test_int8_matmul_of_nothing_gives_the_bias(M, N, dtype):
     assert y.count_nonzero().item() == 0
     b.check_around()
     assert trfn.tr_device_status() == 0
+
+
+@gpu
+def test_errors_of_earlier_calls_are_not_reported():
+    """A transfer station for a device that does not exist leaves the
+    runtime's last error set; no token-row call takes it for its own."""
+    slots = [torch.empty(4096, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((9, 64), generator=g, device="cuda")
+    q, scale = torch.empty(9, 64, dtype=torch.int8, device="cuda"), torch.empty(9, device="cuda")
+    y, out, dx = torch.empty(9, 9, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    dw = torch.empty(64, device="cuda")
+    ws = torch.empty(trfn.tr_rms_norm_backward_workspace_bytes(9, 64), dtype=torch.uint8, device="cuda")
+    big, big_scale = any_int8(g, 9000, 768), torch.ones(9000, device="cuda")
+    big_y = torch.empty(9000, 300, device="cuda")
+    big_ws = torch.empty(trfn.tr_int8_matmul_workspace_bytes(9000, 300, 768), dtype=torch.uint8, device="cuda")
+    for call, launches in ((lambda: trfn.tr_quantize_rows(x, q, scale), 1),
+                           (lambda: trfn.tr_dequantize_rows(q, scale, out), 1),
+                           (lambda: trfn.tr_rms_norm(x, out), 1),
+                           (lambda: trfn.tr_rms_norm_backward(x, x, dx, dweight=dw, workspace=ws), 2),
+                           (lambda: trfn.tr_int8_matmul(q[:1], scale[:1], q, scale, y[:1]), 1),
+                           (lambda: trfn.tr_int8_matmul(q, scale, q, scale, y), 1),
+                           (lambda: trfn.tr_int8_matmul(big, big_scale, big[:300], big_scale[:300], big_y, workspace=big_ws), 2)):
+        trfn.TransferStation(4096, slots, *streams).close()
+        before = trfn.tr_launch_count()
+        call()
+        assert trfn.tr_launch_count() - before == launches
+    torch.cuda.synchronize()
