@@ -3,8 +3,9 @@ functions carry the C entry points' names.
 
 Matrices are 2-D CUDA tensors with unit column stride (any row stride);
 outputs and workspaces are the caller's, as everywhere in this package.  Each
-call enqueues on `stream` (the tensors' device's current one if None) and
-raises TrError on a refusal.
+call enqueues on `stream` (the current one if None) and raises TrError on a
+refusal.  The tensors are on the current device, all of them: the library
+launches there, and a tensor elsewhere is refused.
 """
 from ._native import TrError, check, lib
 
@@ -12,16 +13,17 @@ ELEM_F32, ELEM_F16, ELEM_BF16, ELEM_I8 = 0, 1, 2, 3
 MAX_ROW, MAX_INT8_K = 32768, 131071   # TR_MAX_ROW, TR_MAX_INT8_K
 
 _codes = {}           # torch dtypes, filled when the first tensor comes
-_current_stream = None
+_current_stream = _current_device = None
 
 
 def _prepare():
-    global _current_stream
+    global _current_stream, _current_device
     import torch
     _codes.update({torch.float32: ELEM_F32, torch.float16: ELEM_F16, torch.bfloat16: ELEM_BF16,
                    torch.int8: ELEM_I8})
     # the handle alone: a stream object costs a microsecond a call
     _current_stream = torch._C._cuda_getCurrentRawStream
+    _current_device = torch._C._cuda_getDevice
 
 
 def _elem(t):
@@ -30,42 +32,54 @@ def _elem(t):
     return _codes.get(t.dtype, -1)
 
 
-def _stream(stream, t):
+def _stream(stream, device, where):
+    """The stream's handle, for tensors on this device, which has to be the current one."""
+    if device < 0:
+        raise TrError(1, where, "the tensors must be CUDA tensors")
+    if device != _current_device():
+        raise TrError(1, where, "the tensors are on cuda:%d, the current device is cuda:%d" % (device, _current_device()))
     if stream is None:
-        return _current_stream(t.get_device())
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _matrix(t, shape, elem, where, name):
-    """Address and row stride of a CUDA matrix of this shape and element type."""
+def _elsewhere(t, where, name):
+    return TrError(1, where, "%s %s" % (name, "must be a CUDA tensor" if t.get_device() < 0 else
+                                        "is not on the device of the other tensors"))
+
+
+def _matrix(t, shape, elem, device, where, name):
+    """Address and row stride of a matrix of this shape and element type (any if -1) on this CUDA device."""
     if t.shape != shape:
         raise TrError(1, where, "%s must be a %s matrix" % (name, tuple(shape)))
     if elem >= 0 and _codes.get(t.dtype, -1) != elem:
         raise TrError(1, where, "%s has another type" % name)
-    if not t.is_cuda:
-        raise TrError(1, where, "%s must be a CUDA tensor" % name)
+    if t.get_device() != device:
+        raise _elsewhere(t, where, name)
     row, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise TrError(1, where, "%s must have unit column stride" % name)
     return t.data_ptr(), row
 
 
-def _vector(t, n, where, name):
-    """Address of n contiguous binary32 values; None for None."""
+def _vector(t, n, device, where, name):
+    """Address of n contiguous binary32 values on this CUDA device; None for None."""
     if t is None:
         return None
     if _codes.get(t.dtype, -1) != ELEM_F32 or t.numel() != n or not t.is_contiguous():
         raise TrError(1, where, "%s must be %d contiguous float32 values" % (name, n))
-    if not t.is_cuda:
-        raise TrError(1, where, "%s must be a CUDA tensor" % name)
+    if t.get_device() != device:
+        raise _elsewhere(t, where, name)
     return t.data_ptr()
 
 
-def _workspace(ws, need, where):
+def _workspace(ws, need, device, where):
     if need == 0:
         return None
-    if ws is None or ws.numel() * ws.element_size() < need or not ws.is_cuda or not ws.is_contiguous():
+    if ws is None or ws.numel() * ws.element_size() < need or not ws.is_contiguous():
         raise TrError(1, where, "needs a contiguous CUDA workspace of at least %d bytes" % need)
+    if ws.get_device() != device:
+        raise _elsewhere(ws, where, "workspace")
     return ws.data_ptr()
 
 
@@ -87,13 +101,14 @@ def tr_rms_norm(x, out, weight=None, residual=None, residual_out=None, scale=Non
     shape = _shape(x, where, "x")
     rows, cols = shape
     dt = _elem(x)
-    pr, sr = (None, 0) if residual is None else _matrix(residual, shape, dt, where, "residual")
-    ph, sh = (None, 0) if residual_out is None else _matrix(residual_out, shape, dt, where, "residual_out")
-    px, sx = _matrix(x, shape, dt, where, "x")
-    po, so = _matrix(out, shape, -1, where, "out")
-    rc = lib().tr_rms_norm(px, pr, _vector(weight, cols, where, "weight"), po, ph,
-                           _vector(scale, rows, where, "scale"), rows, cols, sx, sr, so, sh, dt, _elem(out), eps,
-                           _stream(stream, x))
+    device = x.get_device()
+    pr, sr = (None, 0) if residual is None else _matrix(residual, shape, dt, device, where, "residual")
+    ph, sh = (None, 0) if residual_out is None else _matrix(residual_out, shape, dt, device, where, "residual_out")
+    px, sx = _matrix(x, shape, -1, device, where, "x")
+    po, so = _matrix(out, shape, -1, device, where, "out")
+    rc = lib().tr_rms_norm(px, pr, _vector(weight, cols, device, where, "weight"), po, ph,
+                           _vector(scale, rows, device, where, "scale"), rows, cols, sx, sr, so, sh, dt, _elem(out), eps,
+                           _stream(stream, device, where))
     if rc:
         check(rc, where)
 
@@ -115,16 +130,17 @@ def tr_rms_norm_backward(dy, h, dx, weight=None, dweight=None, dresidual=None, e
     shape = _shape(h, where, "h")
     rows, cols = shape
     dt = _elem(h)
-    py, sy = _matrix(dy, shape, dt, where, "dy")
-    ph, sh = _matrix(h, shape, dt, where, "h")
-    px, sx = _matrix(dx, shape, dt, where, "dx")
-    pr, sr = (None, 0) if dresidual is None else _matrix(dresidual, shape, dt, where, "dresidual")
+    device = h.get_device()
+    py, sy = _matrix(dy, shape, dt, device, where, "dy")
+    ph, sh = _matrix(h, shape, -1, device, where, "h")
+    px, sx = _matrix(dx, shape, dt, device, where, "dx")
+    pr, sr = (None, 0) if dresidual is None else _matrix(dresidual, shape, dt, device, where, "dresidual")
     ws = None
     if dweight is not None and rows > 0:
-        ws = _workspace(workspace, lib().tr_rms_norm_backward_workspace_bytes(rows, cols), where)
-    rc = lib().tr_rms_norm_backward(py, ph, _vector(weight, cols, where, "weight"), pr, px,
-                                    _vector(dweight, cols, where, "dweight"), rows, cols, sy, sh, sr, sx, dt, eps,
-                                    ws, _stream(stream, h))
+        ws = _workspace(workspace, lib().tr_rms_norm_backward_workspace_bytes(rows, cols), device, where)
+    rc = lib().tr_rms_norm_backward(py, ph, _vector(weight, cols, device, where, "weight"), pr, px,
+                                    _vector(dweight, cols, device, where, "dweight"), rows, cols, sy, sh, sr, sx, dt, eps,
+                                    ws, _stream(stream, device, where))
     if rc:
         check(rc, where)
 
@@ -136,10 +152,11 @@ def tr_quantize_rows(x, q, scale, stream=None):
     shape = _shape(x, where, "x")
     rows, cols = shape
     dt = _elem(x)
-    pq, sq = _matrix(q, shape, ELEM_I8, where, "q")
-    px, sx = _matrix(x, shape, dt, where, "x")
-    rc = lib().tr_quantize_rows(px, pq, _vector(scale, rows, where, "scale"), rows, cols, sx, sq, dt,
-                                _stream(stream, x))
+    device = x.get_device()
+    pq, sq = _matrix(q, shape, ELEM_I8, device, where, "q")
+    px, sx = _matrix(x, shape, -1, device, where, "x")
+    rc = lib().tr_quantize_rows(px, pq, _vector(scale, rows, device, where, "scale"), rows, cols, sx, sq, dt,
+                                _stream(stream, device, where))
     if rc:
         check(rc, where)
 
@@ -150,10 +167,11 @@ def tr_dequantize_rows(q, scale, out, stream=None):
     shape = _shape(q, where, "q")
     rows, cols = shape
     dt = _elem(out)
-    pq, sq = _matrix(q, shape, ELEM_I8, where, "q")
-    po, so = _matrix(out, shape, -1, where, "out")
-    rc = lib().tr_dequantize_rows(pq, _vector(scale, rows, where, "scale"), po, rows, cols, sq, so, dt,
-                                  _stream(stream, q))
+    device = q.get_device()
+    pq, sq = _matrix(q, shape, ELEM_I8, device, where, "q")
+    po, so = _matrix(out, shape, -1, device, where, "out")
+    rc = lib().tr_dequantize_rows(pq, _vector(scale, rows, device, where, "scale"), po, rows, cols, sq, so, dt,
+                                  _stream(stream, device, where))
     if rc:
         check(rc, where)
 
@@ -173,12 +191,14 @@ def tr_int8_matmul(x, x_scale, w, w_scale, y, bias=None, workspace=None, stream=
     M, K = shape = _shape(x, where, "x")
     N = _shape(w, where, "w")[0]
     dt = _elem(y)
-    px, sx = _matrix(x, shape, ELEM_I8, where, "x")
-    pw, sw = _matrix(w, (N, K), ELEM_I8, where, "w")
-    py, sy = _matrix(y, (M, N), -1, where, "y")
+    device = x.get_device()
+    px, sx = _matrix(x, shape, ELEM_I8, device, where, "x")
+    pw, sw = _matrix(w, (N, K), ELEM_I8, device, where, "w")
+    py, sy = _matrix(y, (M, N), -1, device, where, "y")
     L = lib()
-    ws = _workspace(workspace, L.tr_int8_matmul_workspace_bytes(M, N, K), where)
-    rc = L.tr_int8_matmul(px, _vector(x_scale, M, where, "x_scale"), pw, _vector(w_scale, N, where, "w_scale"),
-                          _vector(bias, N, where, "bias"), py, M, N, K, sx, sw, sy, dt, ws, _stream(stream, x))
+    ws = _workspace(workspace, L.tr_int8_matmul_workspace_bytes(M, N, K), device, where)
+    rc = L.tr_int8_matmul(px, _vector(x_scale, M, device, where, "x_scale"), pw,
+                          _vector(w_scale, N, device, where, "w_scale"), _vector(bias, N, device, where, "bias"), py,
+                          M, N, K, sx, sw, sy, dt, ws, _stream(stream, device, where))
     if rc:
         check(rc, where)

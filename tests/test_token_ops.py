@@ -676,3 +676,83 @@ def test_errors_of_earlier_calls_are_not_reported():
         call()
         assert trfn.tr_launch_count() - before == launches
     torch.cuda.synchronize()
+
+
+class Elsewhere:
+    """Stands in for a contiguous tensor on a GPU of any number."""
+
+    is_cuda = True
+
+    def __init__(self, dtype, *shape, device=0):
+        self.dtype, self.shape, self.device = dtype, torch.Size(shape), device
+
+    def get_device(self):
+        return self.device
+
+    def stride(self):
+        return self.shape[1], 1
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x100000
+
+
+def test_tensors_on_other_devices_are_refused(monkeypatch):
+    """Nothing reaches the library unless every tensor is on the current device."""
+    t = trfn.tokens
+    t._elem(torch.zeros(1))   # fills the module's tables
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return lambda *a: 4096
+            return lambda *a: calls.append(name) or 0
+
+    current = [0]
+    monkeypatch.setattr(t, "lib", Library)
+    monkeypatch.setattr(t, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(t, "_current_device", lambda: current[0], raising=False)
+
+    def f(n=None, device=0):
+        return Elsewhere(torch.float32, *((4, 64) if n is None else (n,)), device=device)
+
+    def i8(device=0):
+        return Elsewhere(torch.int8, 4, 64, device=device)
+
+    def space(device=0):
+        return Elsewhere(torch.uint8, 4096, device=device)
+
+    entries = {
+        "tr_rms_norm": lambda a: t.tr_rms_norm(f(device=a[0]), i8(a[1]), weight=f(64, a[2]), residual=f(device=a[3]),
+                                               residual_out=f(device=a[4]), scale=f(4, a[5])),
+        "tr_rms_norm_backward": lambda a: t.tr_rms_norm_backward(f(device=a[0]), f(device=a[1]), f(device=a[2]), weight=f(64, a[3]),
+                                                                 dweight=f(64, a[4]), dresidual=f(device=a[5]), workspace=space(a[6])),
+        "tr_quantize_rows": lambda a: t.tr_quantize_rows(f(device=a[0]), i8(a[1]), f(4, a[2])),
+        "tr_dequantize_rows": lambda a: t.tr_dequantize_rows(i8(a[0]), f(4, a[1]), f(device=a[2])),
+        "tr_int8_matmul": lambda a: t.tr_int8_matmul(i8(a[0]), f(4, a[1]), i8(a[2]), f(4, a[3]),
+                                                     Elsewhere(torch.float32, 4, 4, device=a[4]), bias=f(4, a[5]), workspace=space(a[6])),
+    }
+    count = {"tr_rms_norm": 6, "tr_rms_norm_backward": 7, "tr_quantize_rows": 3, "tr_dequantize_rows": 3, "tr_int8_matmul": 7}
+    for name, call in entries.items():
+        n = count[name]
+        for device in (0, 1):
+            current[0] = device
+            calls.clear()
+            call([device] * n)   # all on the current device
+            assert calls == [name]
+            for at in range(n):   # one of them elsewhere, or on the CPU
+                for other in (1 - device, -1):
+                    with pytest.raises(TrError):
+                        call([other if i == at else device for i in range(n)])
+            with pytest.raises(TrError, match="current device"):
+                call([1 - device] * n)   # all of them elsewhere
+            assert calls == [name]
