@@ -10,11 +10,15 @@ magnitudes.  An 8-bit value is within a half of its unrounded value, plus 127
 times the relative error of what it is rounded from.  The integer product is
 exact up to its conversion, two scalings and the bias: 4 * 2^-24 of the sum of
 the magnitudes.  Every bound adds the rounding to the output's type."""
+import ctypes
+import os
+import subprocess
+
 import pytest
 import torch
 
 import image_preprocessing_gb300 as trfn
-from image_preprocessing_gb300 import TrError, _native
+from image_preprocessing_gb300 import TrError, _native, build
 
 OK, INVALID, NOT_SUPPORTED = 0, 1, 2
 UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
@@ -756,3 +760,35 @@ def test_tensors_on_other_devices_are_refused(monkeypatch):
             with pytest.raises(TrError, match="current device"):
                 call([1 - device] * n)   # all of them elsewhere
             assert calls == [name]
+
+
+@pytest.fixture(scope="module")
+def early_release(tmp_path_factory):
+    """early_release(out, ns): fills an int8 tensor ns after it has let the next kernel start."""
+    path = str(tmp_path_factory.mktemp("early") / "early_release.so")
+    source = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c_abi", "early_release.cu")
+    subprocess.run([build._nvcc(), "-shared", *build.ARCH, "-O2", "-Xcompiler", "-fPIC", "-o", path, source], check=True)
+    fn = ctypes.CDLL(path).early_release
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_ulonglong, ctypes.c_void_p]
+    return lambda out, ns: fn(out.data_ptr(), out.numel(), ns, torch.cuda.current_stream().cuda_stream)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1, 300, 512), (16, 256, 256), (40, 300, 4096), (196, 512, 1000), (9000, 300, 768)])
+def test_a_long_kernel_before_the_product_does_not_count_as_its_wait(early_release, M, N, K):
+    """The kernel before lets the product start, then runs longer than the
+    limit of the product's waits (1 s) and writes x last of all."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    w = any_int8(g, N, K)
+    ones = torch.ones(max(M, N), device="cuda")
+    y = torch.zeros(M, N, device="cuda")
+    work = torch.empty(trfn.tr_int8_matmul_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert early_release(x, 1_500_000_000) == 0
+    trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=work)
+    torch.cuda.synchronize()
+    filled = (torch.arange(M * K, device="cuda") * 7 % 251 - 125).to(torch.int8).view(M, K)
+    assert torch.equal(x, filled)
+    assert torch.equal(y, product_exact(filled, w).float())
+    assert trfn.tr_device_status() == 0
