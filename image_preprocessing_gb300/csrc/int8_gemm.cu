@@ -160,6 +160,7 @@ struct GemmParams {
     void* y;
     long long y_stride;
     int M, N, k_blocks, m_tiles, n_tiles, wide;   // wide: rows of y take 16-byte stores
+    int missing;                                  // test hook: arrivals that the first stage waits for in vain
 };
 
 // Shared memory: the ring, 2 KB for each epilogue warp, (scale, bias) of two
@@ -192,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     if (threadIdx.x == 0) {
         given_up = 0;
         for (int s = 0; s < ST; ++s) {
-            bar_init(full(s), 1);
+            bar_init(full(s), s == 0 && blockIdx.x == 0 ? 1 + p.missing : 1);
             bar_init(empty(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -247,14 +248,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 for (int i = 0; i < issued; ++i) {
                     s = s == 0 ? ST - 1 : s - 1;
                     if (s == ST - 1) phase ^= 1u;
-                    for (int n = 0; n < (1 << 20) && !bar_try(full(s), phase); ++n) {}
+                    bar_drain(full(s), phase);
                 }
         }
     } else if (warp == 1 && rank == 0) {
+        // the waits for copies are limited from here on, not from when the kernel that makes them still runs
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         constexpr uint32_t shape = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);   // f16 x f16 -> f32, 256 x BN
         const uint64_t x0 = operand(ring), w0 = operand(ring + kBlockBytes);
         int s = 0, half = 0;
         uint32_t phase = 0, half_phase = 0;
+        uint32_t last = 0, last_phase = 0;   // the stage whose products were issued last
         bool ok = true;
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             for (int part = 0; part < parts && ok; ++part) {
@@ -272,17 +276,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                     for (int k = 0; k < kBlockK / 16; ++k)
                         mma_pair(d, x0 + at + 2 * k, w0 + at + 2 * k, shape, kb > kb0 || k > 0);
                     commit_both(empty(s));
+                    last = empty(s);
+                    last_phase = phase;
                     if (++s == ST) { s = 0; phase ^= 1u; }
                 }
+                if (!ok) break;   // these sums are not whole: nobody gets them
                 commit_both(sums_full(half));
                 if (++half == 2) { half = 0; half_phase ^= 1u; }
             }
         }
-        // the last products are done before TMEM is freed: their arrival on sums_full of the half before
-        const int last = half ^ 1;
-        const uint32_t last_phase = half == 0 ? half_phase ^ 1u : half_phase;
-        if (pair < tiles)
-            for (int n = 0; n < (1 << 20) && !bar_try(sums_full(last), last_phase); ++n) {}
+        if (last != 0) bar_drain(last, last_phase);   // the last products are done before TMEM is freed
         __syncwarp();
     } else if (warp >= 4) {
         constexpr int W = BN / 2;                      // channels of a warp
@@ -558,6 +561,7 @@ int launch_int8_gemm(const MatmulArgs& a) {
     p.y = a.y;
     p.y_stride = a.y_stride;
     p.M = a.M; p.N = a.N; p.k_blocks = kb;
+    p.missing = test_waits();
     const int es = a.out_dtype == TR_ELEM_F32 ? 4 : 2;
     p.wide = (uintptr_t)a.y % 16 == 0 && (a.y_stride * es) % 16 == 0;
     if (a.out_dtype == TR_ELEM_F32) return pick_gemm<float>(p, copies, st);

@@ -53,6 +53,7 @@ struct MidParams {
     long long y_stride;
     int tokens, m_tiles, split, blocks;   // of a tile (a multiple of 16), CTAs of a cluster, blocks of K in each
     int wide;                             // groups of 4 channels of y take one store
+    int missing;                          // test hook: arrivals that the first stage waits for in vain
 };
 
 // A stage holds a block in binary16, rows of 128 bytes; the ring holds several in int8, 16 bytes at a time in
@@ -63,6 +64,8 @@ template <int T> constexpr int kSlots = T == 128 ? 1 : 2;                  // st
 template <int T> constexpr int kStages = kGroups<T> * kSlots<T>;
 template <int T> constexpr int kDeep = T == 32 ? 3 : T == 128 ? 1 : 2;     // blocks of the ring for a group
 template <int T> constexpr int kSmemBytes = 1024 + kStages<T> * kStageBytes<T> + kGroups<T> * kDeep<T> * kRingBytes<T>;
+// What a CTA of a cluster gives for sums that a wait has kept it from; the sums themselves stay above -2^31 + 2^14.
+constexpr int kNoSum = INT_MIN;
 constexpr int kPass = kGroup / 4;                                                     // rows of a group's threads
 template <int T> constexpr int kPieces = T < kPass ? 1 : T / kPass;                   // of x, for a thread and block
 
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
         if (lane == 0) {
             given_up = 0;
             for (int s = 0; s < ST; ++s) {
-                bar_init(full(s), kGroup / 32);
+                bar_init(full(s), kGroup / 32 + (s == 0 && blockIdx.x == 0 ? p.missing : 0));
                 bar_init(empty(s), 1);
             }
             bar_init(sums, NI);
@@ -204,6 +207,7 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
         const uint32_t d = tmem + issuer * T;
         int s = issuer * SL, slot_of = 0;   // stages in the order of the blocks: slot 0 of each group, slot 1 ...
         uint32_t phase = 0;
+        uint32_t last = 0, last_phase = 0;        // the stage whose products were issued last
         for (int part = 0; part < parts && ok; ++part) {
             if (part > 0) ok = __all_sync(0xffffffffu, bar_wait(freed, (part - 1) & 1, &given_up, &g_mid_status));
             if (!ok) break;
@@ -217,6 +221,8 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
 #pragma unroll
                 for (int k = 0; k < kBlockK / 16; ++k) mma_one(d, w0 + at + 2 * k, x0 + at + 2 * k, shape, i > i0 || k > 0);
                 commit(empty(s));
+                last = empty(s);
+                last_phase = phase;
                 if constexpr (NI == GR) {        // one group's stages in turn
                     if (++slot_of == SL) { slot_of = 0; phase ^= 1u; }
                     s = issuer * SL + slot_of;
@@ -225,11 +231,9 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
                     if (s >= ST) { s = issuer; phase ^= 1u; }
                 }
             }
-            commit(sums);
-            // after a wait that ran out: what was issued is done before TMEM is freed
-            if (!ok)
-                for (int n = 0; n < (1 << 20) && !bar_try(sums, part & 1); ++n) {}
+            if (ok) commit(sums);   // (else they are not whole: nobody gets them)
         }
+        if (last != 0) bar_drain(last, last_phase);   // what was issued is done before TMEM is freed
         __syncwarp();
     }
 
@@ -348,6 +352,11 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
                 }
             }
             tmem_fence_before();
+        } else if (p.split > 1) {
+            int* const dump = reinterpret_cast<int*>(stages);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                for (int j = 0; j < G && column(u) < p.tokens; ++j) dump[(column(u) + j) * kRows + ch] = kNoSum;
         }
     }
     if (p.split > 1) {
@@ -367,10 +376,13 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
 #pragma unroll
                 for (int r = 0; r < 8; ++r) v[r] = load_peer(at, r, r < p.split);
                 int4 sum = v[0];
+                bool lost = v[0].x == kNoSum;
 #pragma unroll
                 for (int r = 1; r < 8; ++r) {
+                    lost |= v[r].x == kNoSum;
                     sum.x += v[r].x; sum.y += v[r].y; sum.z += v[r].z; sum.w += v[r].w;
                 }
+                if (lost) continue;
                 const float sx = x_scale[token];
                 union { typename std::conditional<sizeof(E) == 4, uint4, uint2>::type word; E e[4]; } o;
                 o.e[0] = out_value<E>((float)sum.x * sx * sw[0] + bias[0]);
@@ -478,6 +490,7 @@ int launch_int8_mid(const MatmulArgs& a) {
     p.bias = a.bias;
     p.y = a.y;
     p.y_stride = a.y_stride;
+    p.missing = test_waits();
     const MidPlan plan = plan_mid(a.M, a.N, a.K);
     p.m_tiles = (int)pieces_of(a.M, plan.T);
     p.tokens = (int)pieces_of(pieces_of(a.M, p.m_tiles), 16) * 16;

@@ -62,6 +62,16 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* given_up, unsigned* status) {
     return bar_try(bar, parity) || bar_wait_slow(bar, parity, given_up, status);
 }
+// The same where a CTA ends, for what is in flight: whatever became of the
+// other threads' waits, and without a word if it runs out.
+static __device__ __noinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; i < (1u << 28) && !bar_try(bar, parity); ++i) {
+        if ((i & 255u) != 0) continue;
+        if (t0 == 0) t0 = now_ns();
+        else if (now_ns() - t0 > kWaitLimitNs) return;
+    }
+}
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 

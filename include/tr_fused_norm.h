@@ -633,7 +633,9 @@ int tr_device_status(int* flags, int clear);
  *                    shared-memory stores (a bank-conflict avoidance for
  *                    layouts whose groups span 64 bytes or more); bit 6 is a
  *                    test hook for the kernels' bounded waits: the first band
- *                    of a batch waits for 16 bytes that never arrive, its waits
+ *                    of a batch waits for 16 bytes that never arrive (and the
+ *                    first stage of an int8 product of three tokens or more for
+ *                    an arrival that never comes), its waits
  *                    run out after about a second, the launch returns with bit 0
  *                    of the device status word set and its output incomplete;
  *                    bit 10 makes the odd-row form write its output tile

@@ -27,6 +27,9 @@
  *     overlap; with different row distances, ranges that cross are refused.
  *   - rows = 0 is no work (a dweight is still written: zeros); cols is at least 1.
  *   - Calls that may run at the same time need workspaces of their own.
+ *   - A product whose pipeline waits for more than about a second sets bit 0 of
+ *     tr_device_status()'s word; parts of its output are then not written, the
+ *     rest is right.
  */
 #ifndef TR_TOKEN_OPS_H
 #define TR_TOKEN_OPS_H

@@ -13,6 +13,7 @@ the magnitudes.  Every bound adds the rounding to the output's type."""
 import ctypes
 import os
 import subprocess
+import time
 
 import pytest
 import torch
@@ -791,4 +792,36 @@ def test_a_long_kernel_before_the_product_does_not_count_as_its_wait(early_relea
     filled = (torch.arange(M * K, device="cuda") * 7 % 251 - 125).to(torch.int8).view(M, K)
     assert torch.equal(x, filled)
     assert torch.equal(y, product_exact(filled, w).float())
+    assert trfn.tr_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(16, 256, 256), (40, 300, 4096), (128, 16384, 640), (600, 384, 20000), (196, 300, 333), (9000, 300, 768),
+                                   (9000, 600, 2100)])
+def test_a_product_whose_wait_runs_out_stores_no_unfinished_sums(M, N, K):
+    """The first stage of the first CTA waits for an arrival that never comes
+    (tr_tune_tiled's test hook): the launch ends by itself and reports it, and
+    what it has written is right."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    x, w = any_int8(g, M, K), any_int8(g, N, K)
+    ones = torch.ones(max(M, N), device="cuda")
+    y = torch.full((M, N), 0.5, device="cuda")   # no sum of integers
+    work = torch.empty(trfn.tr_int8_matmul_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    want = product_exact(x, w).float()
+    assert trfn.tr_device_status(clear=True) == 0
+    try:
+        trfn.tr_tune_tiled(0, 0, 0, 64)
+        t0 = time.perf_counter()
+        trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=work)
+        torch.cuda.synchronize()
+        elapsed = time.perf_counter() - t0
+    finally:
+        trfn.tr_tune_tiled(0, 0, 0, 0)
+    assert 0.5 < elapsed < 30
+    assert trfn.tr_device_status(clear=True) == 1
+    written = y != 0.5
+    assert not bool(written[0, 0])
+    assert torch.equal(y[written], want[written])
+    trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=work)
+    assert torch.equal(y, want)
     assert trfn.tr_device_status() == 0
