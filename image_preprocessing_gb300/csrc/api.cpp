@@ -438,11 +438,10 @@ int tr_validate_aug_params(const tr_aug_param* p, int N, int H, int W, int* bad_
 
 int tr_device_status(int* flags, int clear) {
     if (flags == nullptr) return TR_ERR_INVALID_ARGUMENT;
-    int norm = 0, gemm = 0, mid = 0;
+    int norm = 0, product = 0;
     int rc = read_device_status(&norm, clear != 0);
-    if (rc == TR_OK) rc = read_gemm_status(&gemm, clear != 0);
-    if (rc == TR_OK) rc = read_mid_status(&mid, clear != 0);
-    if (rc == TR_OK) *flags = norm | gemm | mid;
+    if (rc == TR_OK) rc = read_product_status(&product, clear != 0);
+    if (rc == TR_OK) *flags = norm | product;
     return rc;
 }
 

@@ -36,8 +36,6 @@
 namespace trfn {
 namespace {
 
-__device__ unsigned int g_gemm_status;
-
 constexpr int kBlockRows = 128, kBlockK = 64, kBlockBytes = kBlockRows * kBlockK * 2;
 constexpr int kExactBlocks = 1024 / kBlockK;       // blocks of K summed in binary32
 constexpr int kEpilogueWarps = 8;
@@ -161,6 +159,7 @@ struct GemmParams {
     long long y_stride;
     int M, N, k_blocks, m_tiles, n_tiles, wide;   // wide: rows of y take 16-byte stores
     int missing;                                  // test hook: arrivals that the first stage waits for in vain
+    unsigned* status;                             // the product's status word
 };
 
 // Shared memory: the ring, 2 KB for each epilogue warp, (scale, bias) of two
@@ -231,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 const int ch = nt * BN + (int)rank * (BN / 2);
                 const int wb = (ch >> 7) * p.k_blocks, sub = ch & 127;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!bar_wait(empty(s), phase ^ 1u, &given_up, &g_gemm_status)) { ok = false; break; }
+                    if (!bar_wait(empty(s), phase ^ 1u, &given_up, p.status)) { ok = false; break; }
                     const uint32_t at = ring + s * kStageBytes<BN>;
                     // both CTAs' bytes count on the even one's barrier
                     if (rank == 0) bar_expect(full(s), 2 * kStageBytes<BN>);
@@ -262,13 +261,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         bool ok = true;
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             for (int part = 0; part < parts && ok; ++part) {
-                ok = __all_sync(0xffffffffu, bar_wait(sums_empty(half), half_phase ^ 1u, &given_up, &g_gemm_status));
+                ok = __all_sync(0xffffffffu, bar_wait(sums_empty(half), half_phase ^ 1u, &given_up, p.status));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t d = tmem + half * BN;
                 const int kb0 = part * kExactBlocks, kb1 = min(p.k_blocks, kb0 + kExactBlocks);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, &g_gemm_status));
+                    ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, p.status));
                     if (!ok) break;
                     tmem_fence_after();
                     const uint32_t at = s * (kStageBytes<BN> / 16);   // descriptors count in 16 bytes
@@ -320,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             ahead = scales_of(tile + pairs);
             int acc[ONE ? 1 : W];
             for (int part = 0; part < parts - 1; ++part) {
-                ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, &g_gemm_status));
+                ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, p.status));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
@@ -342,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
                 if (lane == 0) bar_arrive_even(sums_empty(half));
                 if (++half == 2) { half = 0; half_phase ^= 1u; }
             }
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, &g_gemm_status));
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait(sums_full(half), half_phase, &given_up, p.status));
             if (!ok) continue;   // to the barrier, where all eight warps leave together
             tmem_fence_after();
             const uint32_t at = tmem + half * BN + col0 + ((uint32_t)(quarter * 32) << 16);
@@ -480,6 +479,8 @@ int start_gemm(const GemmParams& q, const Copies& c, cudaStream_t st) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_failed("cudaGetDevice", (int)e);
+    rc = product_status_word(dev, &p.status);
+    if (rc != TR_OK) return rc;
     std::atomic<int>& pairs = known[dev];
     int n = pairs.load(std::memory_order_relaxed);
     if (n == 0) {
@@ -567,21 +568,6 @@ int launch_int8_gemm(const MatmulArgs& a) {
     if (a.out_dtype == TR_ELEM_F32) return pick_gemm<float>(p, copies, st);
     if (a.out_dtype == TR_ELEM_F16) return pick_gemm<__half>(p, copies, st);
     return pick_gemm<__nv_bfloat16>(p, copies, st);
-}
-
-int read_gemm_status(int* flags, bool clear) {
-    unsigned v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_gemm_status, sizeof v);
-    if (e == cudaSuccess && clear && v != 0) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbol(g_gemm_status, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        set_last_error("tr_device_status (int8 product)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    *flags = (int)v;
-    return TR_OK;
 }
 
 }  // namespace trfn

@@ -32,8 +32,6 @@
 namespace trfn {
 namespace {
 
-__device__ unsigned int g_mid_status;
-
 constexpr int kRows = 128, kBlockK = 64, kExactBlocks = 1024 / kBlockK;
 constexpr int kGroup = 128;                                    // threads of a group
 template <int T> constexpr int kGroups = T == 16 || T == 128 ? 4 : 3;
@@ -54,6 +52,7 @@ struct MidParams {
     int tokens, m_tiles, split, blocks;   // of a tile (a multiple of 16), CTAs of a cluster, blocks of K in each
     int wide;                             // groups of 4 channels of y take one store
     int missing;                          // test hook: arrivals that the first stage waits for in vain
+    unsigned* status;                     // the product's status word
 };
 
 // A stage holds a block in binary16, rows of 128 bytes; the ring holds several in int8, 16 bytes at a time in
@@ -209,12 +208,12 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
         uint32_t phase = 0;
         uint32_t last = 0, last_phase = 0;        // the stage whose products were issued last
         for (int part = 0; part < parts && ok; ++part) {
-            if (part > 0) ok = __all_sync(0xffffffffu, bar_wait(freed, (part - 1) & 1, &given_up, &g_mid_status));
+            if (part > 0) ok = __all_sync(0xffffffffu, bar_wait(freed, (part - 1) & 1, &given_up, p.status));
             if (!ok) break;
             tmem_fence_after();
             const int i0 = part * PART + issuer, i1 = min(nkb, (part + 1) * PART);
             for (int i = i0; i < i1; i += NI) {
-                ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, &g_mid_status));
+                ok = __all_sync(0xffffffffu, bar_wait(full(s), phase, &given_up, p.status));
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t at = s * (kStageBytes<T> / 16);   // descriptors count in 16 bytes
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
         for (int i = group; i < nkb; i += GR) {
             const int k = (kb0 + i) * kBlockK + q * 16;
             if constexpr (ON16) asm volatile("cp.async.wait_group %0;" ::"n"(DEEP - 1) : "memory");
-            ok = __all_sync(0xffffffffu, bar_wait(empty(at), phase, &given_up, &g_mid_status));
+            ok = __all_sync(0xffffffffu, bar_wait(empty(at), phase, &given_up, p.status));
             if (!ok) break;
             uint8_t* const stage = stages + at * kStageBytes<T>;
             auto put = [&](uint8_t* rows, int r, const uint4& v) {
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
                 const int done = i / PART + 1;   // parts converted, when this was the group's last block of one
                 if (i % PART >= PART - GR && done * PART < nkb) {
                     // sums of 1024 products, and more to come
-                    ok = __all_sync(0xffffffffu, bar_wait(sums, (done - 1) & 1, &given_up, &g_mid_status));
+                    ok = __all_sync(0xffffffffu, bar_wait(sums, (done - 1) & 1, &given_up, p.status));
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
             }
         }
         if constexpr (ON16) asm volatile("cp.async.wait_all;" ::: "memory");
-        if (ok && parts > 0) ok = bar_wait(sums, (parts - 1) & 1, &given_up, &g_mid_status);
+        if (ok && parts > 0) ok = bar_wait(sums, (parts - 1) & 1, &given_up, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (tid < p.tokens) x_scale[tid] = my_scale;
         if (tid < kRows) channel[tid] = my_channel;
@@ -413,11 +412,14 @@ __global__ void __launch_bounds__(kThreads<T>, 1) mid_kernel(const MidParams p) 
 long long pieces_of(long long v, long long of) { return (v + of - 1) / of; }
 
 template <typename E, int T, bool ONE, bool ON16>
-int start_mid(const MidParams& p, cudaStream_t st) {
+int start_mid(const MidParams& q, cudaStream_t st) {
+    MidParams p = q;
     static std::atomic<bool> set_up[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_failed("cudaGetDevice", (int)e);
+    const int rc = product_status_word(dev, &p.status);
+    if (rc != TR_OK) return rc;
     std::atomic<bool>& ready = set_up[dev];
     if (!ready.load(std::memory_order_relaxed)) {
         e = cudaFuncSetAttribute(mid_kernel<E, T, ONE, ON16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -507,20 +509,5 @@ int launch_int8_mid(const MatmulArgs& a) {
 }
 
 double int8_mid_cycles(long long M, long long N, long long K) { return plan_mid(M, N, K).cycles; }
-
-int read_mid_status(int* flags, bool clear) {
-    unsigned v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_mid_status, sizeof v);
-    if (e == cudaSuccess && clear && v != 0) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbol(g_mid_status, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        set_last_error("tr_device_status (int8 product)", (int)e);
-        return TR_ERR_CUDA;
-    }
-    *flags = (int)v;
-    return TR_OK;
-}
 
 }  // namespace trfn

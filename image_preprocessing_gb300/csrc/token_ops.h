@@ -82,9 +82,12 @@ int launch_int8_mid(const MatmulArgs& a);
 // Estimates of the two, in SM cycles.
 double int8_gemm_cycles(long long M, long long N, long long K);
 double int8_mid_cycles(long long M, long long N, long long K);
-// Status bits their kernels left on the current device (as read_device_status).
-int read_gemm_status(int* flags, bool clear);
-int read_mid_status(int* flags, bool clear);
+
+// The int8 product's status word (int8_status.cu) on device `dev`, the current
+// one; reading it (as read_device_status, on the current device) copies nothing
+// before the word has been asked for there.
+int product_status_word(int dev, unsigned** word);
+int read_product_status(int* flags, bool clear);
 
 // A failed runtime call as a tr_status: keeps its text for tr_last_error_message, and takes it from the runtime's
 // last error, where another call would find it.

@@ -13,6 +13,7 @@ the magnitudes.  Every bound adds the rounding to the output's type."""
 import ctypes
 import os
 import subprocess
+import sys
 import time
 
 import pytest
@@ -825,3 +826,35 @@ def test_a_product_whose_wait_runs_out_stores_no_unfinished_sums(M, N, K):
     trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=work)
     assert torch.equal(y, want)
     assert trfn.tr_device_status() == 0
+
+
+@gpu
+def test_reading_the_device_status_costs_what_it_did():
+    """In a process without products it is two small copies (the word, and the
+    site of a failed check), no dearer than two elements of a tensor read one
+    by one; products add one copy."""
+    script = """
+import time, torch
+import image_preprocessing_gb300 as trfn
+value = torch.zeros(1, device="cuda")
+def best(call):
+    times = []
+    for _ in range(300):
+        t0 = time.perf_counter()
+        call()
+        times.append(time.perf_counter() - t0)
+    return min(times)
+mean, std, _ = trfn.tr_norm_preset("IMAGENET")
+src = torch.zeros((1, 32, 32, 3), dtype=torch.uint8, device="cuda")
+trfn.tr_fused_norm(src, torch.empty((1, 32, 32, 3), dtype=torch.float16, device="cuda"), mean, std)
+before = best(trfn.tr_device_status) / best(value.item)
+q, one, y = torch.ones(16, 64, dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda"), torch.empty(16, 16, device="cuda")
+trfn.tr_int8_matmul(q, one, q, one, y)
+assert trfn.tr_device_status() == 0 and bool((y == 64).all())
+print(before, best(trfn.tr_device_status) / best(value.item))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    before, after = map(float, r.stdout.split())
+    assert before <= 2 and after <= 3
