@@ -213,7 +213,7 @@ int tr_dequantize_rows(const int8_t* q, const float* scale, void* out, long long
 
 size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K) {
     if (M < 1 || N < 1 || K < 1 || M > kMaxProductRows || N > kMaxProductRows || K > TR_MAX_INT8_K) return 0;
-    return int8_matmul_workspace(M, N, K);
+    return int8_matmul_workspace_up_to(M, N, K);
 }
 
 int tr_int8_matmul(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,

@@ -73,7 +73,9 @@ struct MatmulArgs {
     void* stream;
 };
 int launch_int8_matmul(const MatmulArgs& a);
+// What a product of these sizes needs, and what all of up to M tokens need at most.
 size_t int8_matmul_workspace(long long M, long long N, long long K);
+size_t int8_matmul_workspace_up_to(long long M, long long N, long long K);
 // many tokens (int8_gemm.cu): binary16 copies in the workspace, tcgen05
 int launch_int8_gemm(const MatmulArgs& a);
 size_t int8_gemm_workspace(long long M, long long N, long long K);

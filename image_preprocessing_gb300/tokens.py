@@ -177,6 +177,7 @@ def tr_dequantize_rows(q, scale, out, stream=None):
 
 
 def tr_int8_matmul_workspace_bytes(M, N, K):
+    """Bytes of a workspace for products of up to M tokens with this N and K."""
     return int(lib().tr_int8_matmul_workspace_bytes(M, N, K))
 
 
@@ -186,7 +187,7 @@ def tr_int8_matmul(x, x_scale, w, w_scale, y, bias=None, workspace=None, stream=
 
     x: int8 (M, K), x_scale: M float32; w: int8 (N, K), w_scale: N float32;
     bias: N float32 or None; y: (M, N) float32, float16 or bfloat16; workspace:
-    tr_int8_matmul_workspace_bytes(M, N, K) bytes."""
+    tr_int8_matmul_workspace_bytes(M, N, K) bytes, for this M or a larger one."""
     where = "tr_int8_matmul"
     M, K = shape = _shape(x, where, "x")
     N = _shape(w, where, "w")[0]
@@ -196,9 +197,14 @@ def tr_int8_matmul(x, x_scale, w, w_scale, y, bias=None, workspace=None, stream=
     pw, sw = _matrix(w, (N, K), ELEM_I8, device, where, "w")
     py, sy = _matrix(y, (M, N), -1, device, where, "y")
     L = lib()
-    ws = _workspace(workspace, L.tr_int8_matmul_workspace_bytes(M, N, K), device, where)
+    # the size holds for up to M tokens: this M may do without, which the library knows
+    need = L.tr_int8_matmul_workspace_bytes(M, N, K)
+    given = not need or (workspace is not None and workspace.numel() * workspace.element_size() >= need)
+    ws = _workspace(workspace, need, device, where) if given else None
     rc = L.tr_int8_matmul(px, _vector(x_scale, M, device, where, "x_scale"), pw,
                           _vector(w_scale, N, device, where, "w_scale"), _vector(bias, N, device, where, "bias"), py,
                           M, N, K, sx, sw, sy, dt, ws, _stream(stream, device, where))
     if rc:
+        if rc == 1 and not given:
+            raise TrError(1, where, "needs a contiguous CUDA workspace of at least %d bytes, or another argument is invalid" % need)
         check(rc, where)

@@ -112,7 +112,9 @@ int tr_quantize_rows(const void* x, int8_t* q, float* scale, long long rows, lon
 int tr_dequantize_rows(const int8_t* q, const float* scale, void* out, long long rows, long long cols,
                        long long q_stride, long long out_stride, int dtype, void* stream);
 
-/* Bytes of tr_int8_matmul's workspace (host only; 0 where it needs none).    */
+/* Bytes of a workspace for tr_int8_matmul of up to M tokens with this N and K
+ * (host only; 0 where none of them needs one).  It never shrinks as M grows, so
+ * the largest M's workspace serves all.                                      */
 size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K);
 
 /* tr_int8_matmul — for token m and channel n
@@ -121,8 +123,8 @@ size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K);
  *   w        N x K int8;                            w_scale  N binary32
  *   bias     N binary32, or NULL.
  *   y        M x N of out_dtype (F32, F16 or BF16).
- *   workspace device, tr_int8_matmul_workspace_bytes() bytes, 16-byte aligned,
- *            not initialised; NULL where that is 0.
+ *   workspace device, tr_int8_matmul_workspace_bytes() bytes for this M or a
+ *            larger one, 16-byte aligned, not initialised; NULL where that is 0.
  * The sum is exact in integers; it is rounded to binary32 once, scaled, and
  * rounded to out_dtype.  K = 0 gives the bias (a sum of 0, which scales that
  * are not finite make NaN).

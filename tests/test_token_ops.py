@@ -858,3 +858,31 @@ print(before, best(trfn.tr_device_status) / best(value.item))
     assert r.returncode == 0, r.stderr
     before, after = map(float, r.stdout.split())
     assert before <= 2 and after <= 3
+
+
+def test_int8_matmul_workspace_of_the_largest_batch_serves_all():
+    sizes = trfn.tr_int8_matmul_workspace_bytes
+    for N, K in ((1024, 768), (300, 640), (64, 64), (4096, 4096), (515, 515), (16384, 100), (2048, 131071)):
+        last = 0
+        for M in list(range(1, 5200)) + [50176, 50177, 10 ** 6]:
+            now = sizes(M, N, K)
+            assert now >= last, (M, N, K)
+            last = now
+    assert sizes(1, 16384, 8192) == sizes(2, 16384, 8192) == 0
+
+
+@gpu
+@pytest.mark.parametrize("N,K,largest", [(1024, 768, 2305), (300, 640, 4338), (1024, 1024, 5000)])
+def test_int8_matmul_in_the_workspace_of_the_largest_batch(N, K, largest):
+    """Smaller batches stay inside it, whichever kernels they take."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    size = trfn.tr_int8_matmul_workspace_bytes(largest, N, K)
+    whole = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    w, ones = any_int8(g, N, K), torch.ones(max(N, largest), device="cuda")
+    for M in (3, 200, 1000, 2048, 2304, 2305, 4096, 4337, largest):
+        if M > largest:
+            continue
+        x, y = any_int8(g, M, K), torch.zeros(M, N, device="cuda")
+        trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=whole[:size])
+        assert torch.equal(y, product_exact(x, w).float()), M
+        assert bool((whole[size:] == 0x5A).all())
