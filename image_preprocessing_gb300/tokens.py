@@ -49,15 +49,15 @@ def _elsewhere(t, where, name):
 
 
 def _matrix(t, shape, elem, device, where, name):
-    """Address and row stride of a matrix of this shape and element type (any if -1) on this CUDA device."""
-    if t.shape != shape:
+    """Address and row stride of a matrix of this shape (any if None) and element type (any if -1) on this CUDA device."""
+    if shape is not None and t.shape != shape:
         raise TrError(1, where, "%s must be a %s matrix" % (name, tuple(shape)))
     if elem >= 0 and _codes.get(t.dtype, -1) != elem:
         raise TrError(1, where, "%s has another type" % name)
     if t.get_device() != device:
         raise _elsewhere(t, where, name)
     row, col = t.stride()
-    if col != 1 and shape[1] > 1:
+    if col != 1 and t.shape[1] > 1:
         raise TrError(1, where, "%s must have unit column stride" % name)
     return t.data_ptr(), row
 
@@ -104,7 +104,7 @@ def tr_rms_norm(x, out, weight=None, residual=None, residual_out=None, scale=Non
     device = x.get_device()
     pr, sr = (None, 0) if residual is None else _matrix(residual, shape, dt, device, where, "residual")
     ph, sh = (None, 0) if residual_out is None else _matrix(residual_out, shape, dt, device, where, "residual_out")
-    px, sx = _matrix(x, shape, -1, device, where, "x")
+    px, sx = _matrix(x, None, -1, device, where, "x")
     po, so = _matrix(out, shape, -1, device, where, "out")
     rc = lib().tr_rms_norm(px, pr, _vector(weight, cols, device, where, "weight"), po, ph,
                            _vector(scale, rows, device, where, "scale"), rows, cols, sx, sr, so, sh, dt, _elem(out), eps,
@@ -132,7 +132,7 @@ def tr_rms_norm_backward(dy, h, dx, weight=None, dweight=None, dresidual=None, e
     dt = _elem(h)
     device = h.get_device()
     py, sy = _matrix(dy, shape, dt, device, where, "dy")
-    ph, sh = _matrix(h, shape, -1, device, where, "h")
+    ph, sh = _matrix(h, None, -1, device, where, "h")
     px, sx = _matrix(dx, shape, dt, device, where, "dx")
     pr, sr = (None, 0) if dresidual is None else _matrix(dresidual, shape, dt, device, where, "dresidual")
     ws = None
@@ -154,7 +154,7 @@ def tr_quantize_rows(x, q, scale, stream=None):
     dt = _elem(x)
     device = x.get_device()
     pq, sq = _matrix(q, shape, ELEM_I8, device, where, "q")
-    px, sx = _matrix(x, shape, -1, device, where, "x")
+    px, sx = _matrix(x, None, -1, device, where, "x")
     rc = lib().tr_quantize_rows(px, pq, _vector(scale, rows, device, where, "scale"), rows, cols, sx, sq, dt,
                                 _stream(stream, device, where))
     if rc:
@@ -189,11 +189,11 @@ def tr_int8_matmul(x, x_scale, w, w_scale, y, bias=None, workspace=None, stream=
     bias: N float32 or None; y: (M, N) float32, float16 or bfloat16; workspace:
     tr_int8_matmul_workspace_bytes(M, N, K) bytes, for this M or a larger one."""
     where = "tr_int8_matmul"
-    M, K = shape = _shape(x, where, "x")
+    M, K = _shape(x, where, "x")
     N = _shape(w, where, "w")[0]
     dt = _elem(y)
     device = x.get_device()
-    px, sx = _matrix(x, shape, ELEM_I8, device, where, "x")
+    px, sx = _matrix(x, None, ELEM_I8, device, where, "x")
     pw, sw = _matrix(w, (N, K), ELEM_I8, device, where, "w")
     py, sy = _matrix(y, (M, N), -1, device, where, "y")
     L = lib()
