@@ -45,9 +45,10 @@ struct Mat {
     long long rows, cols, stride;
     int es;
 
+    // first byte and one past the last, for a stride of 0 or more
     uintptr_t lo() const { return (uintptr_t)p; }
     unsigned __int128 hi() const {
-        return (unsigned __int128)lo() + (unsigned __int128)((rows - 1) * stride + cols) * (unsigned)es;
+        return lo() + ((unsigned __int128)(rows - 1) * (unsigned long long)stride + cols) * (unsigned)es;
     }
     bool empty() const { return p == nullptr || rows == 0 || cols == 0; }
     bool aligned() const { return lo() % (unsigned)es == 0; }
@@ -72,7 +73,7 @@ bool overlaps(const Mat& a, const Mat& b) {
 }
 
 bool bad_input(const Mat& m) {
-    return m.p == nullptr || !m.aligned() || m.stride < 0 || m.stride > kMaxStride;
+    return m.p == nullptr || !m.aligned() || m.stride < 0 || m.stride > kMaxStride || m.hi() >> 64 != 0;
 }
 bool bad_output(const Mat& m) { return bad_input(m) || (m.rows > 1 && m.stride < m.cols); }
 

@@ -16,7 +16,7 @@
  *   - Matrices are row-major with unit column stride; *_stride is the distance
  *     of two rows in elements.  Output strides are at least the row's length
  *     (a single row's stride is not looked at); input strides are 0 or more (0
- *     repeats one row).
+ *     repeats one row).  A matrix ends within the address space.
  *   - Pointers are aligned to their element.  Rows whose start and stride are
  *     multiples of 16 bytes are read in 16-byte pieces; any other alignment
  *     gives the same results more slowly.

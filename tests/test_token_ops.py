@@ -684,6 +684,23 @@ def test_errors_of_earlier_calls_are_not_reported():
     torch.cuda.synchronize()
 
 
+def test_matrices_beyond_the_address_space_are_refused():
+    """Rows whose distances add up to 2^64 elements: their ends must not wrap
+    round to where they look harmless."""
+    L = _native.lib()
+    X, Q, S, R, W, H = 1 << 40, 1 << 41, 1 << 42, 1 << 43, 1 << 44, 1 << 45
+    near_by = 64
+    for rows, far in ((2 ** 24 + 1, 2 ** 40), (2 ** 30 + 1, 2 ** 40), (2 ** 30 + 1, 2 ** 34)):
+        assert L.tr_quantize_rows(X, Q, S, rows, 64, far, near_by, 1, None) == INVALID
+        assert L.tr_quantize_rows(X, Q, S, rows, 64, near_by, far, 1, None) == INVALID
+        assert L.tr_dequantize_rows(Q, S, X, rows, 64, far, near_by, 0, None) == INVALID
+        assert L.tr_rms_norm(X, R, None, Q, H, None, rows, 64, near_by, far, near_by, near_by, 1, 1, 1e-6, None) == INVALID
+        assert L.tr_rms_norm(X, R, None, Q, H, None, rows, 64, near_by, near_by, near_by, far, 1, 1, 1e-6, None) == INVALID
+        assert L.tr_rms_norm_backward(X, R, None, None, Q, None, rows, 64, near_by, far, 0, near_by, 1, 1e-6, None, None) == INVALID
+        assert L.tr_int8_matmul(X, S, W, S + (1 << 40), None, Q, rows, 8, 64, far, 64, 8, 0, H, None) == INVALID
+        assert L.tr_int8_matmul(X, S, W, S + (1 << 40), None, Q, 8, rows, 64, 64, far, 2 ** 32, 0, H, None) == INVALID
+
+
 class Elsewhere:
     """Stands in for a contiguous tensor on a GPU of any number."""
 
