@@ -903,3 +903,31 @@ def test_int8_matmul_in_the_workspace_of_the_largest_batch(N, K, largest):
         trfn.tr_int8_matmul(x, ones[:M], w, ones[:N], y, workspace=whole[:size])
         assert torch.equal(y, product_exact(x, w).float()), M
         assert bool((whole[size:] == 0x5A).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=name_of)
+@pytest.mark.parametrize("rows,cols", [(12501, 64), (12501, 257), (15001, 504), (12501, 506), (9003, 511), (12501, 512), (5003, 999),
+                                       (5003, 1024), (3501, 2041), (2001, 4096), (1777, 4095), (901, 8191), (901, 8192), (801, 9001),
+                                       (701, 16384), (501, 20000)])
+def test_rms_norm_backward_through_many_rows(rows, cols, dtype):
+    """Each CTA goes through several rows, past the ones copied ahead at its
+    start: aligned rows, dense rows off 16-byte boundaries, and rows that do
+    not lie alike.  The bounds are those of the sizes above."""
+    b = Buffers(cols + 3)
+    w = 1 + 0.2 * b.randn(cols)
+    ws = torch.empty(trfn.tr_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    ws.fill_(0xFF)
+    h0, dy0, dres0 = b.randn(rows, cols) * 2, b.randn(rows, cols), b.randn(rows, cols)
+    for pads, shift in (((0, 0, 0, 0), 0), ((3, 0, 8, 1), 1)):
+        h, dy, dres = (b.put(v, dtype, pad, shift) for v, pad in zip((h0, dy0, dres0), pads))
+        dx, dw = b.empty(rows, cols, dtype, pads[3], shift), torch.full((cols,), 7.0, device="cuda")
+        trfn.tr_rms_norm_backward(dy, h, dx, weight=w, dweight=dw, dresidual=dres, eps=1e-5, workspace=ws)
+        want, size, want_w, size_w = grad_exact(dy, h, w, dres, 1e-5)
+        near(dx, want, 2.0 ** -17 * size, dtype)
+        near(dw, want_w, (rows + 200) * 2.0 ** -24 * size_w, torch.float32)
+        b.check_around()
+        dense = dx.clone()
+        trfn.tr_rms_norm_backward(dy, h, dres, weight=w, dresidual=dres, eps=1e-5)   # over the residual's gradient
+        assert torch.equal(dres, dense)
+        b.kept.clear()
