@@ -114,6 +114,7 @@ def tr_rms_norm(x, out, weight=None, residual=None, residual_out=None, scale=Non
 
 
 def tr_rms_norm_backward_workspace_bytes(rows, cols):
+    """Bytes of a workspace for the dweight of up to this many rows of this length."""
     return int(lib().tr_rms_norm_backward_workspace_bytes(rows, cols))
 
 

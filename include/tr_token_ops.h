@@ -82,7 +82,9 @@ int tr_rms_norm(const void* x, const void* residual, const float* weight, void* 
                 long long out_stride, long long residual_out_stride, int dtype, int out_dtype, float eps,
                 void* stream);
 
-/* Bytes of tr_rms_norm_backward's workspace for a dweight (host only).       */
+/* Bytes of tr_rms_norm_backward's workspace for a dweight of up to `rows` rows
+ * of this length (host only).  It never shrinks as rows grows; it may as cols
+ * does.                                                                      */
 size_t tr_rms_norm_backward_workspace_bytes(long long rows, long long cols);
 
 /* tr_rms_norm_backward — gradients of tr_rms_norm's y in the input's type.
@@ -95,8 +97,9 @@ size_t tr_rms_norm_backward_workspace_bytes(long long rows, long long cols);
  *   dx           gradient of h, hence of x and of residual alike; may be dy, h
  *                or dresidual.
  *   dweight      cols binary32, overwritten; or NULL.
- *   workspace    device, tr_rms_norm_backward_workspace_bytes() bytes, 16-byte
- *                aligned, not initialised; needed for a dweight only.
+ *   workspace    device, tr_rms_norm_backward_workspace_bytes() bytes for these
+ *                rows or more of this length, 16-byte aligned, not initialised;
+ *                needed for a dweight only.
  * Sums are binary32 in a fixed order: the same call gives the same bits.    */
 int tr_rms_norm_backward(const void* dy, const void* h, const float* weight, const void* dresidual, void* dx,
                          float* dweight, long long rows, long long cols, long long dy_stride, long long h_stride,

@@ -888,6 +888,13 @@ def test_int8_matmul_workspace_of_the_largest_batch_serves_all():
     assert sizes(1, 16384, 8192) == sizes(2, 16384, 8192) == 0
 
 
+def test_gradient_workspace_of_the_most_rows_serves_all():
+    sizes = trfn.tr_rms_norm_backward_workspace_bytes
+    for cols in (1, 64, 511, 512, 513, 1024, 1025, 4096, 8193, 32768):
+        of_rows = [sizes(rows, cols) for rows in list(range(1, 3000)) + [50176, 2 ** 31 - 1]]
+        assert of_rows == sorted(of_rows) and of_rows[0] >= 4 * cols, cols
+
+
 @gpu
 @pytest.mark.parametrize("N,K,largest", [(1024, 768, 2305), (300, 640, 4338), (1024, 1024, 5000)])
 def test_int8_matmul_in_the_workspace_of_the_largest_batch(N, K, largest):
