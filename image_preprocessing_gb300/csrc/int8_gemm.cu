@@ -14,11 +14,11 @@
 // products are read into integer registers while the other half of TMEM
 // takes the next 1024, so the reading is hidden.
 //
-// Measured: 12544 x 4096 x 4096 240 to 249 us, 1690 to 1755 TFLOP/s, of which the copies take
-// 35 us at 5.8 TB/s and the product runs at 1930 TFLOP/s, the rate of a plain
-// binary16 product; 50176 x 1024 x 768 68.7 us, 21 of them copies; 50176 x 4096 x
-// 1024 231 us, 1825 TFLOP/s; outputs off 16 bytes, 7168 x 8749 x 197, 54 us (93
-// with one row stored at a time).  Converting in the product's kernel instead would
+// Measured: 12544 x 4096 x 4096 242 to 256 us, 1645 to 1740 TFLOP/s, by the clock
+// that the power limit leaves; the copies are 34 of them (5.8 TB/s), the product
+// alone runs at 1950 TFLOP/s, the rate of a plain binary16 product; 50176 x 1024 x
+// 768 68 to 69 us, 21 of them copies; 50176 x 4096 x 1024 233 us, 1800 TFLOP/s;
+// outputs off 16 bytes, 7168 x 8749 x 197, 54 us (93 with one row stored at a time).  Converting in the product's kernel instead would
 // put half as much again through shared memory for each block; copying later
 // tokens beside the product of the first measured slower (73 us).
 #include <cuda.h>

@@ -19,8 +19,9 @@ namespace {
 // (__dp4a); the lanes' sums are added by one redux each, the parts' in shared
 // memory.  Integer sums have no order.  __dp4a runs at about 16 lanes a cycle
 // and SM here, so that two tokens take as long as w's bytes and three go to the
-// tensor cores.  Measured: 1 x 4096 x 4096 5.1 us, 1 x 16384 x 4096 14.4 us (4.7
-// TB/s).
+// tensor cores.  Measured: 1 x 4096 x 4096 5.2 us, 1 x 16384 x 4096 14.3 us (4.7
+// TB/s): 1024 CTAs in somewhat over two waves, each of which starts with nothing
+// under way.
 constexpr int kWarps = 8, kRows = 4, kDepth = 2, kStep = 512;
 
 struct FewParams {
@@ -125,8 +126,10 @@ int start_few(const FewParams& p, bool on16, cudaStream_t st) {
 
 template <typename E, int M>
 int part_few(const FewParams& p, bool on16, cudaStream_t st) {
-    // K in 8 parts where the channels alone do not give each SM four CTAs of two
-    // (1 x 4096 x 16384: 15.1 us in 2 parts, 14.8 in 8; 1 x 16384 x 4096: 14.9 and 17.7)
+    // K in 2 parts, 16 channels a CTA, where that gives each SM a CTA; else in 8, 4 channels a CTA.  In 2 and in 8
+    // parts: 1 x 1216 x 4096 2.7 and 1.8 us, 1 x 2432 x 4096 4.5 and 4.7, 1 x 4096 x 4096 5.2 and 6.4, 1 x 16384 x
+    // 4096 14.3 and 17.4.  (A longer K moves the place where they meet, 1 x 4096 x 16384 14.6 and 14.1, a shorter
+    // one back, 1 x 1216 x 1024 1.6 and 1.7.)
     if (p.w.rows >= 152 * kWarps * kRows / 2) return start_few<E, M, 2>(p, on16, st);
     return start_few<E, M, 8>(p, on16, st);
 }

@@ -17,7 +17,8 @@
 // shared memory.  All of these are added as integers, which have no order.
 //
 // Measured: 16 x 16384 x 4096 17.7 us (67 MB of weights: 3.8 TB/s), 64 x 4096 x
-// 4096 10.2 us, 196 x 4096 x 1024 10.4 us.  What is left: a block takes a CTA 380
+// 4096 10.4 us, 196 x 4096 x 1024 10.4 us; rows off 16 bytes, 16 x 16384 x 4095,
+// 38.4 us.  What is left: a block takes a CTA 380
 // cycles where its share of HBM allows 300, and start, first block and epilogue
 // are 8000 cycles whatever the size.
 #include <atomic>
@@ -468,7 +469,9 @@ MidPlan plan_mid(long long M, long long N, long long K) {
     constexpr int tiles[4] = {16, 32, 64, 128}, cost[4] = {380, 430, 520, 1000};
     constexpr int splits[4] = {1, 2, 4, 8}, room[4] = {152, 152, 144, 120};   // CTAs that run at once in such clusters
     const double blocks = std::ceil((double)K / kBlockK), n_tiles = std::ceil((double)N / kRows);
-    const double slow = K % 16 == 0 ? 1.0 : 2.0;   // contiguous rows off 16-byte boundaries
+    // contiguous rows off 16-byte boundaries; that strides put others off them is not known here (16 x 16384 x
+    // 4095 38.4 us, x 4096 17.7)
+    const double slow = K % 16 == 0 ? 1.0 : 2.0;
     for (int i = 0; i < 4; ++i) {
         const double at = std::ceil((double)M / tiles[i]) * n_tiles;
         for (int j = 0; j < 4 && (j == 0 || blocks >= 4 * splits[j]); ++j) {

@@ -18,13 +18,15 @@
 // s = r * stride mod V values into a pack, and lane i's pack holds columns
 // i V - s ... (SHIFT).  Any other alignment goes value by value.
 //
-// Measured (of the 6.68 TB/s copy rate): norm with residual 50176 x 1024
-// binary16 61.3 us (1.00), 12544 x 4096 bfloat16 61.8 us (0.99) and with 8-bit
-// output 54.5 us (0.99); quantisation 50176 x 768 20.6 us (0.84), reading back
-// 18.2 us (0.95); gradients 50176 x 1024 77.5 us (0.79), 12544 x 4096 74.5 us
-// (0.83), where the instructions, 22 a value with the weights' sums, take half of
+// Measured (of the 6.79 TB/s copy rate): norm with residual 50176 x 1024
+// binary16 61.3 us (0.99), 12544 x 4096 bfloat16 61.8 us (0.98) and with 8-bit
+// output 54.4 us (0.97); quantisation 50176 x 768 20.6 us (0.83), reading back
+// 18.2 us (0.93); gradients 50176 x 1024 77.0 us (0.79), 12544 x 4096 74.2 us
+// (0.82), where the instructions, 22 a value with the weights' sums, take half of
 // the issue slots.  With shifted packs the ends of rows cost instructions: norm
-// 50176 x 999 80.7 us (0.74).
+// 50176 x 999 80.7 us (0.73).  Above 8192 values a row has a CTA of 512
+// or 1024 threads, few of which fit an SM: norm 8192 x 16384 bfloat16 184 us (0.86),
+// quantisation 8192 x 16384 binary16 118 us (0.50).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -434,6 +436,11 @@ __device__ __forceinline__ Two mul_two(Two a, Two b) {
 // A thread copies its packs of the next rows into shared memory while it works
 // on this one; they are its own, so no barrier is needed.  kAhead rows ahead:
 // about 100 KB an SM under way, what its share of the HBM rate takes.
+//
+// Above 8192 columns 1024 threads leave 64 registers to a thread, and weights,
+// sums and packs spill (0.5 KB a thread up to 16384 columns, 2.3 to 3.2 KB above,
+// where binary32 rows are not copied ahead either): 8192 x 8192 bfloat16 99 us
+// (0.80 of the copy rate), 8192 x 12288 404 us (0.29), 4096 x 32768 1303 us (0.12).
 template <int V, int T, int NV> constexpr int kRowBytes = V > 1 ? 3 * NV * 16 * kThreads<T> : 0;
 template <int V, int T, int NV>
 constexpr int kAhead = V == 1 ? 0 : (V == 8 ? 3 : 2) * kRowBytes<V, T, NV> <= 200 * 1024 ? (V == 8 ? 3 : 2) : 200 * 1024 / kRowBytes<V, T, NV>;
@@ -792,8 +799,11 @@ int launch_rows(const RowArgs& a) {
 }
 
 int row_grad_parts(long long rows, long long cols) {
-    // the CTAs that 152 SMs hold at once, a row for each of their row groups at least; a multiple of 8, so that
-    // the rows of one are all at the same place in a pack
+    // The CTAs that 152 SMs hold at once, a row for each of their row groups at least; a multiple of 8, so that
+    // the rows of one are all at the same place in a pack.  By the length alone, so that the workspace is known
+    // before the matrices are.  The last lengths up to 512 (506 and more in 16 bits, 510 in binary32) are an
+    // exception: off the boundaries their packs spread over more than 512 places, a CTA has 64 threads and one
+    // row, and a third of the CTAs that fit are launched (50176 x 511 binary16 201 us, x 504 45 us).
     const long long per = cols <= 512 ? 8 : 1;
     const long long want = 152 * (cols <= 512 ? 2 : cols <= 1024 ? 6 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1);
     const long long most = ((rows + per - 1) / per + 7) / 8 * 8;
