@@ -451,6 +451,7 @@ int tr_tune_tiled(int band_bytes, int stages, int max_ctas_per_sm, int flags) {
     if (band_bytes < 0 || stages < 0 || stages > 8 || stages == 1 || max_ctas_per_sm < 0)
         return TR_ERR_INVALID_ARGUMENT;
     tune_tiled(band_bytes, stages, max_ctas_per_sm, flags);
+    set_test_waits((flags & 64) != 0);
     return TR_OK;
 }
 

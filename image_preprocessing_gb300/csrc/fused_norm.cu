@@ -2714,8 +2714,6 @@ int read_device_status(int* flags, bool clear) {
     return TR_OK;
 }
 
-bool test_waits() { return (g_flags.load(std::memory_order_relaxed) & 64) != 0; }
-
 void tune_tiled(int band_bytes, int stages, int ctas_per_sm, int flags) {
     g_flags.store(flags);
     g_band_bytes.store(band_bytes > 0 ? band_bytes : 0);

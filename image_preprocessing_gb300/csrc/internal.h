@@ -107,9 +107,6 @@ int read_device_status(int* flags, bool clear);
 void set_last_error(const char* what, int cuda_error);
 const char* last_error();
 
-// Whether tune_tiled's test hook for bounded waits is on (flags bit 6).
-bool test_waits();
-
 // Tiled-kernel geometry knobs (0 = default).
 void tune_tiled(int band_bytes, int stages, int ctas_per_sm, int flags);
 

@@ -3,11 +3,18 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "token_ops.h"
 
 namespace trfn {
+
+namespace {
+std::atomic<bool> g_test_waits{false};
+}
+void set_test_waits(bool on) { g_test_waits.store(on, std::memory_order_relaxed); }
+bool test_waits() { return g_test_waits.load(std::memory_order_relaxed); }
 
 int cuda_failed(const char* what, int cuda_error) {
     set_last_error(what, cuda_error);

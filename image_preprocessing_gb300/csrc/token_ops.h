@@ -91,6 +91,10 @@ double int8_mid_cycles(long long M, long long N, long long K);
 int product_status_word(int dev, unsigned** word);
 int read_product_status(int* flags, bool clear);
 
+// tr_tune_tiled's test hook for bounded waits (flags bit 6), for the product's.
+void set_test_waits(bool on);
+bool test_waits();
+
 // A failed runtime call as a tr_status: keeps its text for tr_last_error_message, and takes it from the runtime's
 // last error, where another call would find it.
 int cuda_failed(const char* what, int cuda_error);
