@@ -115,6 +115,13 @@ _SIGNATURES = {
     "tr_dequantize_rows": (_i, [_vp] * 3 + [_ll] * 4 + [_i, _vp]),
     "tr_int8_matmul_workspace_bytes": (ctypes.c_size_t, [_ll] * 3),
     "tr_int8_matmul": (_i, [_vp] * 6 + [_ll] * 6 + [_i, _vp, _vp]),
+    "tr_layer_norm": (_i, [_vp] * 7 + [_ll] * 6 + [_i, _i, _f, _vp]),
+    "tr_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [_ll, _ll]),
+    "tr_layer_norm_backward": (_i, [_vp] * 7 + [_ll] * 6 + [_i, _f, _vp, _vp]),
+    "tr_rotary_frequencies": (_i, [_ll, ctypes.c_double, _i, ctypes.c_double, _ll, _vp, _fp]),
+    "tr_rotary": (_i, [_vp] * 4 + [_ll] * 6 + [_i, _i, _f, _i, _vp]),
+    "tr_attention_workspace_bytes": (ctypes.c_size_t, [_ll] * 5),
+    "tr_attention": (_i, [_vp] * 8 + [_ll] * 10 + [_i, _f, _i, _vp, _vp]),
     "tr_device_status": (_i, [ctypes.POINTER(_i), _i]),
     "tr_launch_count": (_u64, []),
     "tr_tune_tiled": (_i, [_i, _i, _i, _i]),

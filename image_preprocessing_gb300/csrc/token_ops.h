@@ -18,6 +18,7 @@ struct RowArgs {
     const void* x;
     const void* residual;      // or null
     const float* weight;       // or null
+    const float* bias;         // layer norm's, or null
     void* out;
     void* residual_out;        // or null
     float* scale;
@@ -29,6 +30,7 @@ struct RowArgs {
     void* stream;
 };
 int launch_rows(const RowArgs& a);
+int launch_layer_norm(const RowArgs& a);   // what: kNorm or kNormQ8
 
 struct RowGradArgs {
     const void* dy;
@@ -37,7 +39,8 @@ struct RowGradArgs {
     const void* dresidual;     // or null
     void* dx;
     float* dweight;            // or null
-    float* partial;            // workspace for a dweight
+    float* dbias;              // layer norm's, or null
+    float* partial;            // workspace for these
     long long rows, dy_stride, h_stride, dresidual_stride, dx_stride;
     int cols;
     float eps;
@@ -47,6 +50,9 @@ struct RowGradArgs {
 int launch_row_grad(const RowGradArgs& a);
 // CTAs of the gradient kernel, each with one partial dweight row.
 int row_grad_parts(long long rows, long long cols);
+int launch_layer_norm_grad(const RowGradArgs& a);
+// At most this many CTAs, each with a partial row of 2 cols.
+int layer_norm_grad_parts(long long rows, long long cols);
 
 struct DequantArgs {
     const int8_t* q;
@@ -58,6 +64,42 @@ struct DequantArgs {
     void* stream;
 };
 int launch_dequant(const DequantArgs& a);
+
+struct RotaryArgs {
+    const void* x;
+    void* out;
+    const int32_t* positions;  // or null: the row's number
+    const double* freqs;       // host
+    long long tokens, x_stride, out_stride;
+    int heads, dim, rot;
+    int dtype;
+    bool halves, inverse;
+    float magnitude;
+    void* stream;
+};
+int launch_rotary(const RotaryArgs& a);
+
+// Attention; the arrays are on the device.
+struct AttentionArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    const int32_t* q_starts;
+    const int32_t* k_starts;
+    const int32_t* q_lengths;  // or null
+    const int32_t* k_lengths;  // or null
+    int q_rows, k_rows, sequences;
+    int heads, kv_heads, dim;
+    long long q_stride, k_stride, v_stride, out_stride;
+    int dtype;
+    float scale;
+    bool causal;
+    void* workspace;
+    void* stream;
+};
+int launch_attention(const AttentionArgs& a);
+size_t attention_workspace(long long q_rows, long long sequences, long long heads, long long kv_heads, long long dim);
 
 struct MatmulArgs {
     const int8_t* x;

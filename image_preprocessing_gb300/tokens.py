@@ -7,11 +7,16 @@ call enqueues on `stream` (the current one if None) and raises TrError on a
 refusal.  The tensors are on the current device, all of them: the library
 launches there, and a tensor elsewhere is refused.
 """
+import ctypes
+
 from ._native import TrError, check, lib
 
 ELEM_F32, ELEM_F16, ELEM_BF16, ELEM_I8 = 0, 1, 2, 3
 MAX_ROW, MAX_INT8_K = 32768, 131071   # TR_MAX_ROW, TR_MAX_INT8_K
+ROTARY_HALVES, ROTARY_PAIRS = 0, 1
+ROTARY_UNSCALED, ROTARY_LINEAR, ROTARY_BASE, ROTARY_PARTS = 0, 1, 2, 3
 
+_INT32 = 4            # no tr_elem: positions and sequences
 _codes = {}           # torch dtypes, filled when the first tensor comes
 _current_stream = _current_device = None
 
@@ -20,7 +25,7 @@ def _prepare():
     global _current_stream, _current_device
     import torch
     _codes.update({torch.float32: ELEM_F32, torch.float16: ELEM_F16, torch.bfloat16: ELEM_BF16,
-                   torch.int8: ELEM_I8})
+                   torch.int8: ELEM_I8, torch.int32: _INT32})
     # the handle alone: a stream object costs a microsecond a call
     _current_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
@@ -60,6 +65,17 @@ def _matrix(t, shape, elem, device, where, name):
     if col != 1 and t.shape[1] > 1:
         raise TrError(1, where, "%s must have unit column stride" % name)
     return t.data_ptr(), row
+
+
+def _integers(t, n, device, where, name):
+    """Address of n contiguous int32 values on this CUDA device; None for None."""
+    if t is None:
+        return None
+    if _codes.get(t.dtype, -1) != _INT32 or t.numel() != n or not t.is_contiguous():
+        raise TrError(1, where, "%s must be %d contiguous int32 values" % (name, n))
+    if t.get_device() != device:
+        raise _elsewhere(t, where, name)
+    return t.data_ptr()
 
 
 def _vector(t, n, device, where, name):
@@ -146,6 +162,57 @@ def tr_rms_norm_backward(dy, h, dx, weight=None, dweight=None, dresidual=None, e
         check(rc, where)
 
 
+def tr_layer_norm(x, out, weight=None, bias=None, residual=None, residual_out=None, scale=None, eps=1e-5, stream=None):
+    """h = x + residual; out = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) * weight + bias, row by row.
+
+    bias: cols float32, or None for zeros; the others as tr_rms_norm's."""
+    where = "tr_layer_norm"
+    shape = _shape(x, where, "x")
+    rows, cols = shape
+    dt = _elem(x)
+    device = x.get_device()
+    pr, sr = (None, 0) if residual is None else _matrix(residual, shape, dt, device, where, "residual")
+    ph, sh = (None, 0) if residual_out is None else _matrix(residual_out, shape, dt, device, where, "residual_out")
+    px, sx = _matrix(x, None, -1, device, where, "x")
+    po, so = _matrix(out, shape, -1, device, where, "out")
+    rc = lib().tr_layer_norm(px, pr, _vector(weight, cols, device, where, "weight"), _vector(bias, cols, device, where, "bias"),
+                             po, ph, _vector(scale, rows, device, where, "scale"), rows, cols, sx, sr, so, sh, dt, _elem(out),
+                             eps, _stream(stream, device, where))
+    if rc:
+        check(rc, where)
+
+
+def tr_layer_norm_backward_workspace_bytes(rows, cols):
+    """Bytes of a workspace for the dweight and dbias of up to this many rows of this length."""
+    return int(lib().tr_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def tr_layer_norm_backward(dy, h, dx, weight=None, dweight=None, dbias=None, dresidual=None, eps=1e-5, workspace=None,
+                           stream=None):
+    """Gradients of tr_layer_norm's out (in h's type) at h, as tr_rms_norm_backward's.
+
+    dweight, dbias: cols float32 each, overwritten, or None; either needs a
+    workspace of tr_layer_norm_backward_workspace_bytes(rows, cols) bytes."""
+    where = "tr_layer_norm_backward"
+    shape = _shape(h, where, "h")
+    rows, cols = shape
+    dt = _elem(h)
+    device = h.get_device()
+    py, sy = _matrix(dy, shape, dt, device, where, "dy")
+    ph, sh = _matrix(h, None, -1, device, where, "h")
+    px, sx = _matrix(dx, shape, dt, device, where, "dx")
+    pr, sr = (None, 0) if dresidual is None else _matrix(dresidual, shape, dt, device, where, "dresidual")
+    ws = None
+    if (dweight is not None or dbias is not None) and rows > 0:
+        ws = _workspace(workspace, lib().tr_layer_norm_backward_workspace_bytes(rows, cols), device, where)
+    rc = lib().tr_layer_norm_backward(py, ph, _vector(weight, cols, device, where, "weight"), pr, px,
+                                      _vector(dweight, cols, device, where, "dweight"),
+                                      _vector(dbias, cols, device, where, "dbias"), rows, cols, sy, sh, sr, sx, dt, eps, ws,
+                                      _stream(stream, device, where))
+    if rc:
+        check(rc, where)
+
+
 def tr_quantize_rows(x, q, scale, stream=None):
     """Rows of x (float32, float16, bfloat16) in 8 bits: q int8 of x's shape,
     scale rows float32; q * scale stands for x."""
@@ -208,4 +275,91 @@ def tr_int8_matmul(x, x_scale, w, w_scale, y, bias=None, workspace=None, stream=
     if rc:
         if rc == 1 and not given:
             raise TrError(1, where, "needs a contiguous CUDA workspace of at least %d bytes, or another argument is invalid" % need)
+        check(rc, where)
+
+
+def tr_rotary_frequencies(rot, base=10000.0, scaling=ROTARY_UNSCALED, factor=1.0, trained=0):
+    """(freqs, magnitude) for tr_rotary: rot / 2 frequencies (a ctypes array of
+    doubles, radians for each position) and what the turned values are scaled by.
+
+    scaling: for contexts `factor` times as long as the `trained` positions:
+    ROTARY_LINEAR, ROTARY_BASE or ROTARY_PARTS."""
+    where = "tr_rotary_frequencies"
+    if rot < 2 or rot > 512:   # (the size of the array)
+        raise TrError(1 if rot < 2 else 2, where, "rot is between 2 and 512")
+    freqs, magnitude = (ctypes.c_double * (rot // 2))(), ctypes.c_float()
+    rc = lib().tr_rotary_frequencies(rot, base, scaling, factor, trained, freqs, ctypes.byref(magnitude))
+    if rc:
+        check(rc, where)
+    return freqs, magnitude.value
+
+
+def tr_rotary(x, out, heads, freqs, positions=None, layout=ROTARY_HALVES, magnitude=1.0, inverse=False, stream=None):
+    """Rotary positions of every head of x (tokens, heads * dim), into out (may be x).
+
+    freqs: of tr_rotary_frequencies, or a sequence of numbers: a head's first
+    2 * len(freqs) values turn, the rest are copied; positions: tokens int32, or
+    None for 0, 1, ...; inverse: turns back, which is the gradient (dx of dout)."""
+    where = "tr_rotary"
+    shape = _shape(x, where, "x")
+    tokens, cols = shape
+    if heads < 1 or cols % heads:
+        raise TrError(1, where, "x must have heads * dim columns")
+    dt = _elem(x)
+    device = x.get_device()
+    px, sx = _matrix(x, None, -1, device, where, "x")
+    po, so = _matrix(out, shape, dt, device, where, "out")
+    if not isinstance(freqs, ctypes.Array) or freqs._type_ is not ctypes.c_double:
+        freqs = (ctypes.c_double * len(freqs))(*freqs)
+    rc = lib().tr_rotary(px, po, _integers(positions, tokens, device, where, "positions"), freqs, tokens, heads, cols // heads,
+                         2 * len(freqs), sx, so, dt, layout, magnitude, bool(inverse), _stream(stream, device, where))
+    if rc:
+        check(rc, where)
+
+
+def tr_attention_workspace_bytes(q_rows, sequences, heads, kv_heads, dim):
+    """Bytes of a workspace for attention of up to this many rows of q and sequences."""
+    return int(lib().tr_attention_workspace_bytes(q_rows, sequences, heads, kv_heads, dim))
+
+
+def tr_attention(q, k, v, out, heads, kv_heads, q_starts, k_starts=None, q_lengths=None, k_lengths=None, causal=False,
+                 scale=None, workspace=None, stream=None):
+    """Attention of packed sequences, head by head.
+
+    q, out: (rows, heads * dim), k, v: (rows, kv_heads * dim), of one type
+    (float32, float16 or bfloat16); q_starts: sequences + 1 int32, sequence s is
+    the rows q_starts[s] .. q_starts[s + 1], or with q_lengths (sequences int32)
+    the first so many from q_starts[s] on; k_starts, k_lengths: of the keys and
+    values (None, None: those of the queries).  causal: the last query sees every
+    key, the one before it all but the last, and so on.  scale: None for
+    1 / sqrt(dim); workspace: tr_attention_workspace_bytes(...) bytes."""
+    where = "tr_attention"
+    shape = _shape(q, where, "q")
+    rows, cols = shape
+    if heads < 1 or cols % heads or kv_heads < 1 or heads % kv_heads:
+        raise TrError(1, where, "q must have heads * dim columns, heads a multiple of kv_heads")
+    dim = cols // heads
+    dt = _elem(q)
+    device = q.get_device()
+    k_rows = _shape(k, where, "k")[0]
+    pq, sq = _matrix(q, None, -1, device, where, "q")
+    pk, sk = _matrix(k, (k_rows, kv_heads * dim), dt, device, where, "k")
+    pv, sv = _matrix(v, (k_rows, kv_heads * dim), dt, device, where, "v")
+    po, so = _matrix(out, shape, dt, device, where, "out")
+    if k_starts is None:
+        if k_lengths is not None:
+            raise TrError(1, where, "k_lengths needs k_starts")
+        k_starts, k_lengths = q_starts, q_lengths
+    sequences = q_starts.numel() - 1
+    if sequences < 0:
+        raise TrError(1, where, "q_starts must hold sequences + 1 values")
+    qs = _integers(q_starts, sequences + 1, device, where, "q_starts")
+    ks = _integers(k_starts, sequences + 1, device, where, "k_starts")
+    ql = _integers(q_lengths, sequences, device, where, "q_lengths")
+    kl = _integers(k_lengths, sequences, device, where, "k_lengths")
+    L = lib()
+    ws = _workspace(workspace, L.tr_attention_workspace_bytes(rows, sequences, heads, kv_heads, dim), device, where)
+    rc = L.tr_attention(pq, pk, pv, po, qs, ks, ql, kl, rows, k_rows, sequences, heads, kv_heads, dim, sq, sk, sv, so, dt,
+                        dim ** -0.5 if scale is None else scale, bool(causal), ws, _stream(stream, device, where))
+    if rc:
         check(rc, where)

@@ -5,10 +5,16 @@
  *   tr_rms_norm            residual addition and root-mean-square norm, output in
  *                          the input's type or in 8 bits with a scale per row
  *   tr_rms_norm_backward   its gradients
+ *   tr_layer_norm          the same with layer norm, which takes the mean away and
+ *                          adds a bias
+ *   tr_layer_norm_backward its gradients
  *   tr_quantize_rows       8-bit rows with a scale per row (patches, weights)
  *   tr_dequantize_rows     reads them back
  *   tr_int8_matmul         product of two 8-bit matrices with a scale for each
  *                          token and each channel
+ *   tr_rotary              rotary positions of heads, and back (the gradient);
+ *                          tr_rotary_frequencies makes their frequencies
+ *   tr_attention           attention over packed sequences, grouped heads
  *
  * Conventions: those of tr_fused_norm.h (tr_status codes, host checks before
  * anything is launched, caller-owned buffers, no allocation, asynchronous on
@@ -106,6 +112,35 @@ int tr_rms_norm_backward(const void* dy, const void* h, const float* weight, con
                          long long dresidual_stride, long long dx_stride, int dtype, float eps, void* workspace,
                          void* stream);
 
+/* tr_layer_norm — with h = x + residual (h = x without one), for each row
+ *     y_c = (h_c - m) * w_c / sqrt(mean_c((h_c - m)^2) + eps) + b_c,   m = mean_c(h_c)
+ *   bias         cols binary32, or NULL for zeros; the others as tr_rms_norm's.
+ * h, its mean, the squares (of values less the mean) and y are formed in
+ * binary32 and rounded once per output; y is made from the unrounded h.
+ * Errors: those of tr_rms_norm.                                             */
+int tr_layer_norm(const void* x, const void* residual, const float* weight, const float* bias, void* out,
+                  void* residual_out, float* scale, long long rows, long long cols, long long x_stride,
+                  long long residual_stride, long long out_stride, long long residual_out_stride, int dtype,
+                  int out_dtype, float eps, void* stream);
+
+/* Bytes of tr_layer_norm_backward's workspace for the dweight and dbias of up to
+ * `rows` rows of this length (host only).  It never shrinks as rows grows.     */
+size_t tr_layer_norm_backward_workspace_bytes(long long rows, long long cols);
+
+/* tr_layer_norm_backward — gradients of tr_layer_norm's y in the input's type.
+ * With s = 1 / sqrt(mean_c((h_c - m)^2) + eps), u_c = (h_c - m) * s, g_c = dy_c * w_c:
+ *     dx_c = s * (g_c - mean_c(g_c) - u_c * mean_c(g_c * u_c)) + dresidual_c
+ *     dweight_c = sum over rows of dy_c * u_c,   dbias_c = sum over rows of dy_c
+ *   dweight, dbias  cols binary32 each, overwritten; or NULL, either of them.
+ *   workspace    device, tr_layer_norm_backward_workspace_bytes() bytes for these
+ *                rows or more of this length, 16-byte aligned, not initialised;
+ *                needed for a dweight or a dbias only.
+ * The rest as tr_rms_norm_backward.                                         */
+int tr_layer_norm_backward(const void* dy, const void* h, const float* weight, const void* dresidual, void* dx,
+                           float* dweight, float* dbias, long long rows, long long cols, long long dy_stride,
+                           long long h_stride, long long dresidual_stride, long long dx_stride, int dtype, float eps,
+                           void* workspace, void* stream);
+
 /* tr_quantize_rows — 8-bit rows (above) of x: q rows x cols int8, scale rows
  * binary32.                                                                 */
 int tr_quantize_rows(const void* x, int8_t* q, float* scale, long long rows, long long cols, long long x_stride,
@@ -135,6 +170,94 @@ size_t tr_int8_matmul_workspace_bytes(long long M, long long N, long long K);
 int tr_int8_matmul(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
                    const float* bias, void* y, long long M, long long N, long long K, long long x_stride,
                    long long w_stride, long long y_stride, int out_dtype, void* workspace, void* stream);
+
+/* Rotary positions.  The pairs of a head: value k with value k + rot/2, or
+ * value 2k with value 2k + 1.                                               */
+typedef enum tr_rotary_layout { TR_ROTARY_HALVES = 0, TR_ROTARY_PAIRS = 1 } tr_rotary_layout;
+
+/* How frequencies are scaled for contexts `factor` times as long.           */
+typedef enum tr_rotary_scaling {
+    TR_ROTARY_UNSCALED = 0,   /* f_k = base^(-2k / rot) */
+    TR_ROTARY_LINEAR = 1,     /* f_k / factor: positions interpolated */
+    TR_ROTARY_BASE = 2,       /* base * factor^(rot / (rot - 2)): the last pair interpolated, the first kept */
+    TR_ROTARY_PARTS = 3       /* by the turns r_k = trained * f_k / 2 pi that a pair makes over the positions it was
+                               * trained on (the YaRN paper): with g_k = (r_k - 1) / (32 - 1) cut to [0, 1],
+                               * f_k * (g_k + (1 - g_k) / factor), and magnitude 0.1 ln(factor) + 1 */
+} tr_rotary_scaling;
+
+/* Most turned values of a head, heads of a matrix; longest head of attention. */
+#define TR_MAX_ROTARY 512
+#define TR_MAX_HEADS 65535
+#define TR_MAX_HEAD_DIM 256
+
+/* Frequencies of rot/2 pairs, radians for each position, and the magnitude that
+ * goes with them (host only).  trained: for TR_ROTARY_PARTS.
+ * Errors: TR_ERR_INVALID_ARGUMENT for an odd rot or one below 2 (4 for
+ * TR_ROTARY_BASE), base <= 1, factor < 1, trained < 1 where it counts;
+ * TR_ERR_NOT_SUPPORTED for rot > TR_MAX_ROTARY.                             */
+int tr_rotary_frequencies(long long rot, double base, int scaling, double factor, long long trained, double* freqs,
+                          float* magnitude);
+
+/* tr_rotary — for token i, every head and pair k, with t = positions[i]:
+ *     (a, b) -> magnitude * (a cos(t f_k) - b sin(t f_k), b cos(t f_k) + a sin(t f_k))
+ *   x, out       tokens x (heads * dim) of dtype (F32, F16 or BF16): head h is
+ *                columns h * dim ... ; out may be x.
+ *   positions    tokens int32 on the device, any value; or NULL: token i is at i.
+ *   freqs        rot / 2 finite frequencies on the HOST, read before the call
+ *                returns (a captured call keeps them).
+ *   rot          turned values of a head, its first; even, up to dim.  The rest
+ *                are copied.
+ *   inverse      not 0: turns by -t f_k, which is the gradient: dx of dout.
+ * Angles are exact to 2^-24 of a half turn at any position; the products are
+ * binary32, rounded once.
+ * TR_ERR_NOT_SUPPORTED for rot > TR_MAX_ROTARY, heads > TR_MAX_HEADS, dim >
+ * TR_MAX_ROW or tokens > 2^31 - 1.                                          */
+int tr_rotary(const void* x, void* out, const int32_t* positions, const double* freqs, long long tokens, long long heads,
+              long long dim, long long rot, long long x_stride, long long out_stride, int dtype, int layout,
+              float magnitude, int inverse, void* stream);
+
+/* Most rows of q or k, and most sequences, of tr_attention.                 */
+#define TR_MAX_ATTENTION_ROWS 2147483647
+#define TR_MAX_SEQUENCES 1048576
+
+/* Bytes of tr_attention's workspace for up to this many rows of q and sequences
+ * (host only; 0 where none of them needs one).  It never shrinks as either grows. */
+size_t tr_attention_workspace_bytes(long long q_rows, long long sequences, long long heads, long long kv_heads,
+                                    long long dim);
+
+/* tr_attention — for query i and head h of a sequence,
+ *     o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * (q . k_j)),
+ * over the keys j of the sequence that the query sees: all of its Lk keys, or,
+ * causal, the first i + 1 + Lk - Lq of them (the last query sees all: a step's new
+ * tokens come after what is cached).  A query that sees no key gets zeros.
+ *   q, out       q_rows x (heads * dim) of dtype (F32, F16 or BF16): head h is
+ *                columns h * dim ... ;  k, v  k_rows x (kv_heads * dim).  Heads
+ *                h with the same h / (heads / kv_heads) share a key head.
+ *   q_starts     sequences + 1 int32 on the device: sequence s's queries are rows
+ *                q_starts[s] .. q_starts[s + 1]; with q_lengths (sequences int32,
+ *                or NULL) q_starts[s] .. q_starts[s] + q_lengths[s], and what lies
+ *                between is left as it is.  k_starts, k_lengths: keys and values,
+ *                likewise (slots of a cache, filled in part).
+ * Sequences may be empty, keys shared by several.  The arrays are read by the
+ * GPU: nothing outside q, k and v is read whatever they hold (rows beyond a
+ * matrix, or ends before starts, are cut off), and rows of q that belong to
+ * two sequences get either's output.  Rows that belong to none are not written.
+ *   workspace    device, tr_attention_workspace_bytes() bytes for these rows and
+ *                sequences or more, 16-byte aligned, not initialised.
+ * Scores, maxima, sums and outputs are binary32; in F16 and BF16 a weight p is
+ * rounded to dtype for the product with v.  What a query does not see does not
+ * reach its output, whatever it holds (infinities and NaN included).  The same
+ * call gives the same bits.
+ * Fast for F16 and BF16 with dim a multiple of 8 up to 128, up to 64 heads to a
+ * key head, and matrices and strides on 16 bytes; a plain kernel takes the rest.
+ * TR_ERR_INVALID_ARGUMENT where heads is no multiple of kv_heads or out overlaps
+ * another buffer; TR_ERR_NOT_SUPPORTED for dim > TR_MAX_HEAD_DIM, heads >
+ * TR_MAX_HEADS, sequences > TR_MAX_SEQUENCES or rows > TR_MAX_ATTENTION_ROWS. */
+int tr_attention(const void* q, const void* k, const void* v, void* out, const int32_t* q_starts,
+                 const int32_t* k_starts, const int32_t* q_lengths, const int32_t* k_lengths, long long q_rows,
+                 long long k_rows, long long sequences, long long heads, long long kv_heads, long long dim,
+                 long long q_stride, long long k_stride, long long v_stride, long long out_stride, int dtype,
+                 float scale, int causal, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }
