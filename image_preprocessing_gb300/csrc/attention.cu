@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kPlainThreads) plain_kernel(const PlainParams 
     int seen[4], most = 0;   // keys of this thread's rows, and of the tile's
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        seen[r] = row0 + ty * 4 + r < rows ? keys_seen((int)((row0 + ty * 4 + r) / p.group), rq.length, rk.length, p.causal) : 0;
+        seen[r] = row0 + ty * 4 + r < rows ? attention::keys_seen((int)((row0 + ty * 4 + r) / p.group), rq.length, rk.length, p.causal) : 0;
     const long long last = min(row0 + kTile, rows) - 1;
-    most = keys_seen((int)(last / p.group), rq.length, rk.length, p.causal);
+    most = attention::keys_seen((int)(last / p.group), rq.length, rk.length, p.causal);
     float m[4], l[4], o[4][DC];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -210,11 +210,12 @@ int type_plain(const PlainParams& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_workspace(long long q_rows, long long sequences, long long heads, long long kv_heads, long long dim) {
-    return 0;
+size_t attention_workspace(long long q_rows, long long, long long heads, long long kv_heads, long long dim) {
+    return attention_tc_workspace(q_rows, heads, kv_heads, dim);
 }
 
 int launch_attention(const AttentionArgs& a) {
+    if (attention_tc_supported(a)) return launch_attention_tc(a);
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     PlainParams p{a.q, a.k, a.v, a.out,
                   Sequences{a.q_starts, a.k_starts, a.q_lengths, a.k_lengths, a.q_rows, a.k_rows, a.sequences},

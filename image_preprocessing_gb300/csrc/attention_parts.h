@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include "attention_plan.h"
 #include "token_ops.h"
 
 namespace trfn {
@@ -17,13 +18,6 @@ __device__ __forceinline__ Range range_of(const int32_t* starts, const int32_t* 
     return Range{at, (int)min(max(end, (long long)at), (long long)rows) - at};
 }
 
-// Keys that query i of lq sees of lk: the first so many.
-__device__ __forceinline__ int keys_seen(int i, int lq, int lk, bool causal) {
-    if (!causal) return lk;
-    const long long n = (long long)i + 1 + lk - lq;
-    return (int)max(0LL, min(n, (long long)lk));
-}
-
 struct Sequences {
     const int32_t* q_starts;
     const int32_t* k_starts;
@@ -35,6 +29,6 @@ struct Sequences {
 // tcgen05 attention (attention_tc.cu), where it applies.
 bool attention_tc_supported(const AttentionArgs& a);
 int launch_attention_tc(const AttentionArgs& a);
-size_t attention_tc_workspace(long long q_rows, long long sequences, long long heads, long long kv_heads, long long dim);
+size_t attention_tc_workspace(long long q_rows, long long heads, long long kv_heads, long long dim);
 
 }  // namespace trfn

@@ -1,0 +1,977 @@
+// Attention on the tensor cores: binary16 and bfloat16, heads of up to 128 values
+// on 16-byte boundaries (attention.cu has the mathematics and the plain kernel).
+//
+// A CTA on each SM goes through its share of the work (attention_plan.h).  An item
+// is two tiles of 128 rows (queries x heads of one key head) over blocks of 128
+// keys.  Warps: one copies (TMA: queries, then keys and values through a ring of
+// stages) and says what comes next; one issues the products; two make values that
+// a row does not see harmless; four for each tile do the softmax, a thread a row.
+//     S = Q K^T into TMEM; a row's thread reads it, keeps maximum and sum, writes
+//     P = 2^(x - m) in 16 bits over S; O += P V in TMEM, P read from there.
+// The tiles take turns: the tensor cores multiply for one while the other's
+// weights are made.  O is multiplied by 2^(m_old - m_new) only where the maximum
+// has grown by more than 8 (2^8 more in P is no loss: the sum is binary32); the
+// thread does that itself, so there is no correction in the usual block.
+//
+// P is rounded to the type of v, half a unit relative to itself, as the products
+// take it; in binary16 the weights are made 2^6 times as large, so that the ones
+// below 2^-14 of the largest keep more of their bits.
+//
+// What a row does not see: its weight is an exact zero, but 0 times an infinity is
+// not.  In blocks that some row does not see whole, values that are not finite are
+// replaced by zeros in shared memory, and a tile that meets such a block adds them
+// at the end to the rows that do see them.  Keys need no care: their scores are
+// replaced.
+//
+// A share that begins or ends inside an item leaves its sums, maxima and outputs
+// in the workspace, and a second kernel joins them in the order of the keys.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cmath>
+#include <mutex>
+
+#include "attention_parts.h"
+#include "tensor_core.h"
+
+namespace trfn {
+namespace {
+
+using attention::Border;
+using attention::kKeys;
+using attention::kRows;
+
+constexpr int kCtas = 152;                    // one on each SM
+constexpr int kThreads = 384;
+constexpr int kPieces = 8, kFlags = 16;       // descriptors on their way; items whose values may be under way
+constexpr int kBoxRows = 64;                  // keys to a copy
+constexpr float kGrowth = 8.0f;               // of a maximum, in powers of two, before O is multiplied
+
+// What a CTA does of one item, as the copying warp tells the others.
+struct Piece {
+    int q0, tokens;      // its first query's row, and queries
+    int head;            // key head
+    int k0, keys;        // the sequence's first key's row, and keys
+    int base;            // keys that its first query sees (before the bounds); causal: one more for each query
+    int j0, j1;          // blocks of this piece; j0 < 0: nothing follows
+    int n0, n1;          // blocks that the tiles' rows see
+    int slot;            // partial result, or -1
+    int pad[5];
+};
+static_assert(sizeof(Piece) == 64, "pieces of the workspace and of shared memory");
+
+// A partial result in the workspace.
+struct Slot {
+    int state;           // 0 (none), kFirst (of an item) or kNext; kFailed is added by a CTA that gave up
+    int ends;            // the item's last
+    int q0, tokens, head, keys, base, pad;
+};
+constexpr int kFirst = 1, kNext = 2, kFailed = 4;
+
+struct TcParams {
+    CUtensorMap q, k, v;
+    Sequences seq;
+    void* out;
+    const void* values;       // v, for values that are not finite
+    long long out_stride, v_stride;
+    int kv_heads, group, dim, tokens;   // tokens: queries of a tile
+    float scale;              // with log2(e), positive
+    bool causal;
+    Slot* slots;              // 2 kCtas
+    float2* stats;            // 2 kCtas x slot_rows: maximum, sum
+    float* parts;             // 2 kCtas x slot_rows x D
+    int slot_rows;
+    int missing;              // test hook: arrivals that the first stage waits for in vain
+    unsigned* status;
+};
+
+// ------------------------------------------------------------- PTX forms ---
+
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int c, int head, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c), "r"(head), "r"(row), "r"(bar)
+        : "memory");
+}
+// Issued by the whole warp for its one elected thread.
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(shape), "r"(add)
+        : "memory");
+}
+// A in TMEM, two 16-bit values to a column.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(shape), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Values of rows along K (shared memory: 64 of them to a row of 128 bytes, swizzled; 16 KB between
+// the next 64, 1 KB between groups of 8 rows): the matrix is read transposed.
+__device__ __forceinline__ uint64_t operand_across(uint32_t addr, uint32_t apart) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(apart >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+          "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+        "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float power2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <typename E> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Not 0 where one of the two values is not finite: x * 0 is then NaN.
+template <typename E> __device__ __forceinline__ uint32_t not_finite2(uint32_t x);
+template <> __device__ __forceinline__ uint32_t not_finite2<__half>(uint32_t x) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0)));
+    return *reinterpret_cast<const uint32_t*>(&v) & 0x7fff7fffu;
+}
+template <> __device__ __forceinline__ uint32_t not_finite2<__nv_bfloat16>(uint32_t x) {
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
+    return *reinterpret_cast<const uint32_t*>(&v) & 0x7fff7fffu;
+}
+__device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
+__device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The exponent of the type is all ones: one value.
+template <typename E> constexpr uint32_t kExponent = 0x7c00;
+template <> constexpr uint32_t kExponent<__nv_bfloat16> = 0x7f80;
+// Powers of two by which weights are made larger.
+template <typename E> constexpr float kLift = 6.0f;
+template <> constexpr float kLift<__nv_bfloat16> = 0.0f;
+
+// ------------------------------------------------------------- the layout ---
+
+// Shared memory, D = 64 or 128: queries of two tiles (kQ of them), the ring, 4 KB for each softmax warp.
+template <int D> constexpr int kTileBytes = kRows * D * 2;    // of queries, of a block of keys or values
+template <int D> constexpr int kQ = D == 64 ? 2 : 1;
+template <int D> constexpr int kStages = D == 64 ? 7 : 4;
+template <int D> constexpr int kSmem = 1024 + kQ<D> * 2 * kTileBytes<D> + kStages<D> * kTileBytes<D> + 8 * 4096;
+
+__device__ __forceinline__ int seen_by(const Piece& p, bool causal, int token) {
+    if (!causal) return p.keys;
+    const long long n = (long long)p.base + token;
+    return (int)max(0LL, min(n, (long long)p.keys));
+}
+// Whether some row does not see the whole of block j.
+__device__ __forceinline__ bool masked(const Piece& p, bool causal, int j) { return (long long)(j + 1) * kKeys > seen_by(p, causal, 0); }
+
+__device__ __forceinline__ attention::Sequence sequence_of(const TcParams& p, int s) {
+    return attention::Sequence{range_of(p.seq.q_starts, p.seq.q_lengths, s, p.seq.q_rows).length,
+                               range_of(p.seq.k_starts, p.seq.k_lengths, s, p.seq.k_rows).length, p.tokens, p.causal};
+}
+
+// Sum over the CTA's threads before this one, and of all.
+__device__ __forceinline__ long long block_before(long long v, long long* warps, long long& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long left = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += left;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = upto;
+    __syncthreads();
+    long long before = 0;
+    all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warps[w];
+        all += warps[w];
+    }
+    return before + upto - v;
+}
+
+// Borders c and c + 1 of this call's shares, in shared memory.
+__device__ __forceinline__ void find_borders(const TcParams& p, long long* warps, Border* found) {
+    const int n = p.seq.count;
+    long long mine = 0, units = 0;
+    for (int s = threadIdx.x; s < n; s += kThreads) mine += sequence_of(p, s).head_units() * p.kv_heads;
+    block_before(mine, warps, units);
+    // at least two blocks to a CTA
+    const int parts = (int)max(1LL, min((long long)kCtas, units / 2));
+    const int c = blockIdx.x;
+    const long long want[2] = {attention::share_start(units, parts, min(c, parts)), attention::share_start(units, parts, min(c + 1, parts))};
+    if (threadIdx.x < 2) found[threadIdx.x] = Border{units, n, 0, 0, 0};
+    __syncthreads();
+    long long before = 0;
+    for (int s0 = 0; s0 < n && before <= want[1] && before < units; s0 += kThreads) {
+        const int s = s0 + threadIdx.x;
+        attention::Sequence q{0, 0, p.tokens, p.causal};
+        if (s < n) q = sequence_of(p, s);
+        const long long w = n <= kThreads ? mine : q.head_units() * p.kv_heads;
+        long long all = 0;
+        const long long at = before + block_before(w, warps, all);
+        for (int b = 0; b < 2; ++b)
+            if (want[b] >= at && want[b] < at + w)
+                found[b] = attention::border_in(q, s, p.kv_heads, at, want[b], units, parts);
+        before += all;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------- the kernel ---
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ TcParams p) {
+    constexpr int ST = kStages<D>, NQ = kQ<D>, COLS = D / 64;
+    constexpr uint32_t kTypes = sizeof(E) == 2 && kExponent<E> == 0x7f80 ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t kShape = (1u << 4) | kTypes | ((kRows / 16) << 24);   // binary32 sums, 128 rows
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) Piece pieces[kPieces];
+    __shared__ __align__(8) uint64_t bars[3 * ST + 2 * NQ + 2 * kPieces + 6];
+    __shared__ long long warp_sums[kThreads / 32];
+    __shared__ Border borders[2];
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int given_up;
+    __shared__ volatile int not_finite[kFlags];   // the item (by number of pieces) in whose masked blocks values were replaced
+    uint8_t* const base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t queries = smem_u32(base), ring = queries + NQ * 2 * kTileBytes<D>;
+    uint8_t* const passes = base + NQ * 2 * kTileBytes<D> + ST * kTileBytes<D>;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (ST + s); };
+    auto q_full = [&](int s) { return bar0 + 8u * (2 * ST + s); };
+    auto q_empty = [&](int s) { return bar0 + 8u * (2 * ST + NQ + s); };
+    auto piece_full = [&](int s) { return bar0 + 8u * (2 * ST + 2 * NQ + s); };
+    auto piece_empty = [&](int s) { return bar0 + 8u * (2 * ST + 2 * NQ + kPieces + s); };
+    auto scores = [&](int t) { return bar0 + 8u * (2 * ST + 2 * NQ + 2 * kPieces + t); };       // S of tile t is there
+    auto weights = [&](int t) { return bar0 + 8u * (2 * ST + 2 * NQ + 2 * kPieces + 2 + t); };  // P of tile t is there
+    auto summed = [&](int t) { return bar0 + 8u * (2 * ST + 2 * NQ + 2 * kPieces + 4 + t); };   // P V is in O of tile t
+    auto clean = [&](int s) { return bar0 + 8u * (2 * ST + 2 * NQ + 2 * kPieces + 6 + s); };    // values of masked blocks are finite
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        given_up = 0;
+        for (int s = 0; s < ST; ++s) {
+            bar_init(full(s), s == 0 && blockIdx.x == 0 ? 1 + p.missing : 1);
+            bar_init(empty(s), 1);
+            bar_init(clean(s), 2);
+        }
+        for (int s = 0; s < NQ; ++s) {
+            bar_init(q_full(s), 1);
+            bar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < kPieces; ++s) {
+            bar_init(piece_full(s), 1);
+            bar_init(piece_empty(s), 11);   // the products' warp, two that clean, eight softmax warps
+        }
+        for (int t = 0; t < 2; ++t) {
+            bar_init(scores(t), 1);
+            bar_init(weights(t), 4);
+            bar_init(summed(t), 1);
+        }
+        for (int i = 0; i < kFlags; ++i) not_finite[i] = -1;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_fence_before();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel before may make any of what is read here
+    find_borders(p, warp_sums, borders);
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+    auto s_at = [&](int t) { return tmem + t * kKeys; };
+    auto o_at = [&](int t) { return tmem + 2 * kKeys + t * D; };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, &given_up, p.status); };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, &given_up, p.status)) != 0; };
+    // The piece with this number, once it is there; the warp is done with its place then.
+    auto next_piece = [&](int number, Piece& to) {
+        const int s = number % kPieces;
+        if (!wait_all(piece_full(s), (number / kPieces) & 1)) return false;
+        to = pieces[s];
+        __syncwarp();
+        if (lane == 0) arrive(piece_empty(s));
+        return to.j0 >= 0;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            Border b = borders[0];
+            long long left = borders[1].unit - b.unit;
+            // nothing of an earlier call is left in the slots
+            Slot slot[2] = {};
+            int number = 0, item = 0;   // pieces, and those with blocks
+            int s = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            auto stage = [&](const CUtensorMap* map, const Piece& c, int j) {
+                ok = ok && wait(empty(s), phase ^ 1u);
+                if (!ok) return;
+                const int boxes = min(kKeys, c.keys - j * kKeys) > kBoxRows ? 2 : 1;
+                const uint32_t at = ring + s * kTileBytes<D>;
+                bar_expect(full(s), boxes * COLS * kBoxRows * 128);
+                for (int col = 0; col < COLS; ++col)
+                    for (int r = 0; r < boxes; ++r)
+                        box_load(at + col * (kKeys * 128) + r * (kBoxRows * 128), map, col * 64, c.head, c.k0 + j * kKeys + r * kBoxRows,
+                                 full(s));
+                issued = issued < ST ? issued + 1 : ST;
+                if (++s == ST) { s = 0; phase ^= 1u; }
+            };
+            while (left > 0 && ok) {
+                while (b.s < p.seq.count && range_of(p.seq.q_starts, p.seq.q_lengths, b.s, p.seq.q_rows).length == 0) ++b.s;
+                if (b.s >= p.seq.count) break;   // (not reached: what is left lies in some sequence)
+                const Range rq = range_of(p.seq.q_starts, p.seq.q_lengths, b.s, p.seq.q_rows);
+                const Range rk = range_of(p.seq.k_starts, p.seq.k_lengths, b.s, p.seq.k_rows);
+                const attention::Sequence q{rq.length, rk.length, p.tokens, p.causal};
+                while (left > 0 && ok && b.head < p.kv_heads) {
+                    const attention::Step step = attention::next_step(q, b, left);
+                    Piece c;
+                    const int i0 = step.item * 2 * p.tokens;
+                    c.q0 = rq.start + i0;
+                    c.tokens = min(2 * p.tokens, rq.length - i0);
+                    c.head = step.head;
+                    c.k0 = rk.start;
+                    c.keys = rk.length;
+                    c.base = (int)((long long)i0 + 1 + rk.length - rq.length);
+                    c.n0 = step.n0;
+                    c.n1 = step.n1;
+                    c.j0 = step.j0;
+                    c.j1 = step.j1;
+                    c.slot = -1;
+                    if (!step.begins || !step.ends) {
+                        const int which = step.begins ? 1 : 0;
+                        c.slot = 2 * blockIdx.x + which;
+                        slot[which] = Slot{step.begins ? kFirst : kNext, step.ends, c.q0, c.tokens, c.head, c.keys, c.base, 0};
+                    }
+                    ok = wait(piece_empty(number % kPieces), ((number / kPieces) & 1) ^ 1u);
+                    if (!ok) break;
+                    pieces[number % kPieces] = c;
+                    arrive(piece_full(number % kPieces));
+                    ++number;
+                    if (c.j1 > c.j0) {
+                        const int qs = item % NQ;
+                        ok = wait(q_empty(qs), ((item / NQ) & 1) ^ 1u);
+                        if (!ok) break;
+                        const int tiles = c.tokens > p.tokens ? 2 : 1;
+                        bar_expect(q_full(qs), tiles * COLS * p.tokens * p.group * 128);
+                        for (int t = 0; t < tiles; ++t)
+                            for (int col = 0; col < COLS; ++col)
+                                box_load(queries + (qs * 2 + t) * kTileBytes<D> + col * (kRows * 128), &p.q, col * 64, c.head * p.group,
+                                         c.q0 + t * p.tokens, q_full(qs));
+                        ++item;
+                        for (int j = c.j0; j < c.j1 && ok; ++j) {
+                            stage(&p.k, c, j);
+                            stage(&p.v, c, j);
+                        }
+                    }
+                }
+                b.head = 0;
+                ++b.s;
+            }
+            if (ok && wait(piece_empty(number % kPieces), ((number / kPieces) & 1) ^ 1u)) {
+                pieces[number % kPieces].j0 = -1;
+                arrive(piece_full(number % kPieces));
+            }
+            p.slots[2 * blockIdx.x] = slot[0];
+            p.slots[2 * blockIdx.x + 1] = slot[1];
+            // copies in flight land before the CTA ends, whatever became of the others
+            for (int i = 0; i < issued; ++i) {
+                s = s == 0 ? ST - 1 : s - 1;
+                if (s == ST - 1) phase ^= 1u;
+                bar_drain(full(s), phase);
+            }
+            for (int i = item < NQ ? 0 : item - NQ; i < item; ++i) bar_drain(q_full(i % NQ), (i / NQ) & 1);
+        }
+    } else if (warp == 1) {
+        int s = 0, number = 0, item = 0;
+        uint32_t phase = 0, weights_phase[2] = {0, 0};
+        uint32_t last = 0, last_phase = 0;   // the stage whose products were issued last
+        auto advance = [&] {
+            commit(empty(s));
+            last = empty(s);
+            last_phase = phase;
+            if (++s == ST) { s = 0; phase ^= 1u; }
+        };
+        // the next piece that has blocks
+        auto with_blocks = [&](Piece& to) {
+            do {
+                if (!next_piece(number, to)) return false;
+                ++number;
+            } while (to.j1 <= to.j0);
+            return true;
+        };
+        const uint32_t n_values = (uint32_t)(p.dim + 15) / 16, k_steps = n_values;
+        auto end_of = [](const Piece& c, int t) { return min(c.j1, t == 0 ? c.n0 : c.n1); };
+        // keys of block j that some row of tile t sees
+        auto columns = [&](const Piece& c, int t, int j) {
+            const int token = min(c.tokens, (t + 1) * p.tokens) - 1;
+            return min(kKeys, seen_by(c, p.causal, token) - j * kKeys);
+        };
+        auto score = [&](const Piece& c, int t, int j, int qs, int stage) {
+            const uint64_t a = operand(queries + (qs * 2 + t) * kTileBytes<D>), b = operand(ring + stage * kTileBytes<D>);
+            const uint32_t n = (uint32_t)(columns(c, t, j) + 15) / 16;
+            for (uint32_t k = 0; k < k_steps; ++k) {
+                const uint32_t at = (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2;   // 64 values lie 16 KB from the next
+                mma_shared(s_at(t), a + at, b + at, kShape | (2 * n << 17), k > 0);
+            }
+            commit(scores(t));
+        };
+        auto weigh = [&](const Piece& c, int t, int j, int stage) {
+            const uint64_t b = operand_across(ring + stage * kTileBytes<D>, kKeys * 128);
+            const int steps = (columns(c, t, j) + 15) / 16;
+            for (int k = 0; k < steps; ++k)
+                mma_tmem(o_at(t), s_at(t) + k * 8, b + k * (16 * 128 / 16), kShape | (1u << 16) | (2 * n_values << 17), j > c.j0 || k > 0);
+            commit(summed(t));
+        };
+        Piece cur, nxt;
+        bool ok = with_blocks(cur);
+        if (ok) {
+            ok = wait_all(q_full(0), 0) && wait_all(full(s), phase);
+            if (ok) {
+                tmem_fence_after();
+                for (int t = 0; t < 2; ++t)
+                    if (cur.j0 < end_of(cur, t)) score(cur, t, cur.j0, 0, s);
+                advance();
+                if (cur.j0 + 1 == cur.j1) commit(q_empty(0));
+            }
+        }
+        while (ok) {
+            bool more = false;
+            for (int j = cur.j0; j < cur.j1 && ok; ++j) {
+                const int v_stage = s;
+                ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
+                if (!ok) break;
+                // the block whose scores come next: this piece's, or the first of the next one
+                const bool inside = j + 1 < cur.j1;
+                more = inside || with_blocks(nxt);
+                const Piece& then = inside ? cur : nxt;
+                const int then_j = inside ? j + 1 : nxt.j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
+                const int k_stage = s + 1 == ST ? 0 : s + 1;
+                const uint32_t k_phase = s + 1 == ST ? phase ^ 1u : phase;
+                bool there = false;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j < end_of(cur, t)) {
+                        ok = wait_all(weights(t), weights_phase[t]);
+                        weights_phase[t] ^= 1u;
+                        if (!ok) break;
+                        tmem_fence_after();
+                        weigh(cur, t, j, v_stage);
+                    }
+                    if (more && then_j < end_of(then, t)) {
+                        if (!there) {
+                            ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
+                            if (!ok) break;
+                            tmem_fence_after();
+                            there = true;
+                        }
+                        score(then, t, then_j, qs, k_stage);
+                    }
+                }
+                if (!ok) break;
+                advance();
+                if (more) {
+                    advance();
+                    if (then_j + 1 == then.j1) commit(q_empty(qs));
+                }
+            }
+            if (!more) break;
+            cur = nxt;
+            ++item;
+        }
+        if (last != 0) bar_drain(last, last_phase);   // the last products are done before TMEM is freed
+        __syncwarp();
+    } else if (warp < 4) {
+        // Values that a row does not see: rows of the ring beyond the keys become zeros, values that are not finite too.
+        // (The products wait for these warps at every block of values, so neither is ever a turn of the ring ahead.)
+        const int me = threadIdx.x - 64;
+        int s = 0, number = 0;
+        uint32_t phase = 0;
+        Piece c;
+        bool ok = true;
+        auto done = [&] {
+            __syncwarp();
+            if (lane == 0) arrive(clean(s));
+            if (++s == ST) { s = 0; phase ^= 1u; }
+        };
+        while (ok && next_piece(number, c)) {
+            bool found = false;
+            for (int j = c.j0; j < c.j1 && ok; ++j) {
+                ok = wait_all(full(s), phase);   // keys
+                if (!ok) break;
+                done();
+                ok = wait_all(full(s), phase);
+                if (!ok) break;
+                if (masked(c, p.causal, j)) {
+                    uint8_t* const at = base + NQ * 2 * kTileBytes<D> + s * kTileBytes<D>;
+                    const int rows = min(kKeys, c.keys - j * kKeys), whole = (rows + 15) / 16 * 16;
+                    bool wrote = false;
+                    for (int col = 0; col < COLS; ++col)
+                        for (int i = me; i < whole * 8; i += 64) {   // 16 bytes
+                            uint4* const v = reinterpret_cast<uint4*>(at + col * (kKeys * 128)) + i;
+                            if (i >= rows * 8) {
+                                *v = make_uint4(0, 0, 0, 0);
+                                wrote = true;
+                                continue;
+                            }
+                            const uint4 x = *v;
+                            if ((not_finite2<E>(x.x) | not_finite2<E>(x.y) | not_finite2<E>(x.z) | not_finite2<E>(x.w)) == 0) continue;
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                if ((w[h] & kExponent<E>) == kExponent<E>) w[h] &= 0xffff0000u;
+                                if ((w[h] >> 16 & kExponent<E>) == kExponent<E>) w[h] &= 0xffffu;
+                            }
+                            *v = make_uint4(w[0], w[1], w[2], w[3]);
+                            wrote = found = true;
+                        }
+                    if (found) not_finite[number % kFlags] = number;
+                    if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                done();
+            }
+            ++number;
+        }
+    } else {
+        const int tile = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        uint8_t* const pass = passes + (warp - 4) * 4096;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16, s_mine = s_at(tile) + lanes, o_mine = o_at(tile) + lanes;
+        const int token = row / p.group, member = row - token * p.group;
+        uint32_t scores_phase = 0, products = 0;   // products of P and V so far
+        int number = 0;
+        Piece c;
+        bool ok = true;
+        while (ok && next_piece(number, c)) {
+            const int here = tile * p.tokens + token;   // of the item's queries
+            const bool mine = token < p.tokens && here < c.tokens;
+            const bool some = __any_sync(0xffffffffu, mine), tile_has = c.tokens > tile * p.tokens;
+            const int seen = mine ? seen_by(c, p.causal, here) : 0;
+            const int last_seen = seen_by(c, p.causal, min(c.tokens, (tile + 1) * p.tokens) - 1);
+            const int e = min(c.j1, tile == 0 ? c.n0 : c.n1);
+            float ms = -INFINITY, l = 0.0f;   // the maximum times the scale, less the lift
+            for (int j = c.j0; j < e; ++j) {
+                ok = wait_all(scores(tile), scores_phase);
+                scores_phase ^= 1u;
+                if (!ok) break;
+                tmem_fence_after();
+                if (some) {
+                    const int cols = min(kKeys, last_seen - j * kKeys);   // of the tile
+                    uint32_t x[kKeys];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if (g * 32 < cols) tmem_load32(s_mine + g * 32, x + g * 32);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) asm volatile("" : "+r"(x[i]));
+                    if (masked(c, p.causal, j)) {
+                        const int sees = seen - j * kKeys;
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i) x[i] = i < sees ? x[i] : 0xff800000u;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            top[u] = fmaxf(top[u], fmaxf(__uint_as_float(x[i + 2 * u]), __uint_as_float(x[i + 2 * u + 1])));
+                    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale - kLift<E>;
+                    const bool grows = high > ms + kGrowth;
+                    if (__any_sync(0xffffffffu, grows)) {
+                        const float factor = grows ? power2(ms - high) : 1.0f;   // (from -infinity: 0)
+                        if (grows) {
+                            ms = high;
+                            l *= factor;
+                        }
+                        if (j > c.j0) {
+                            ok = wait_all(summed(tile), (products - 1) & 1);
+                            if (!ok) break;
+                            tmem_fence_after();
+#pragma unroll
+                            for (int g = 0; g < D; g += 16) {
+                                uint32_t o[16];
+                                tmem_load16(o_mine + g, o);
+                                tmem_wait(o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                                tmem_store16(o_mine + g, o);
+                            }
+                        }
+                    }
+                    const float off = ms == -INFINITY ? 0.0f : ms;   // nothing seen yet: weights 0
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (g * 64 >= cols) continue;
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) {
+                            const float a = power2(fmaf(__uint_as_float(x[g * 64 + i]), p.scale, -off));
+                            const float b = power2(fmaf(__uint_as_float(x[g * 64 + i + 1]), p.scale, -off));
+                            sum[i & 2] += a;
+                            sum[(i & 2) + 1] += b;
+                            w[i / 2] = pack2<E>(a, b);
+                        }
+                        tmem_store32(s_mine + g * 32, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_stored();
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(weights(tile));
+                ++products;
+            }
+            if (!ok) break;
+            if (tile_has && some) {
+                const bool any = e > c.j0;
+                if (any) {
+                    ok = wait_all(summed(tile), (products - 1) & 1);
+                    if (!ok) break;
+                    tmem_fence_after();
+                }
+                const bool repair = any && not_finite[number % kFlags] == number;
+                const bool whole = c.slot < 0;
+                const long long part = (long long)max(c.slot, 0) * p.slot_rows + tile * kRows;
+                if (!whole && mine) p.stats[part + row] = make_float2(any ? ms : -INFINITY, any ? l : 0.0f);
+                const float inverse = !whole ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
+                // where this row goes, for the lanes that write it
+                const long long to = (long long)(c.q0 + here) * p.out_stride + ((long long)c.head * p.group + member) * p.dim;
+                if (whole || any) {
+                    const int width = whole ? 64 : 32;   // values of 128 bytes
+                    for (int g = 0; g < p.dim; g += 32) {
+                        uint32_t o[32];
+                        if (any) {
+                            tmem_load32(o_mine + g, o);
+                            tmem_wait(o);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = any && seen > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
+                        if (repair && mine) {
+                            // values of masked blocks that are not finite, for the rows that see them
+                            const int from = max(c.j0, seen_by(c, p.causal, 0) / kKeys) * kKeys, until = min(seen, e * kKeys);
+                            for (int k = from; k < until; ++k) {
+                                const E* v = static_cast<const E*>(p.values) + (long long)(c.k0 + k) * p.v_stride + (long long)c.head * p.dim + g;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (g + i < p.dim) {
+                                        const float f = value_of(v[i]);
+                                        if (!isfinite(f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
+                                    }
+                            }
+                        }
+                        // through the warp's 4 KB, so that rows are written in runs of 128 bytes; 16-byte piece q of
+                        // row r lies at q ^ (r & 7): no bank conflicts
+                        uint4* const line = reinterpret_cast<uint4*>(pass) + lane * 8;
+                        if (whole) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                line[((g / 8 & 4) + q) ^ (lane & 7)] =
+                                    make_uint4(pack2<E>(__uint_as_float(o[q * 8]), __uint_as_float(o[q * 8 + 1])),
+                                               pack2<E>(__uint_as_float(o[q * 8 + 2]), __uint_as_float(o[q * 8 + 3])),
+                                               pack2<E>(__uint_as_float(o[q * 8 + 4]), __uint_as_float(o[q * 8 + 5])),
+                                               pack2<E>(__uint_as_float(o[q * 8 + 6]), __uint_as_float(o[q * 8 + 7])));
+                            if (g % 64 == 0 && g + 32 < p.dim) continue;   // the line's other half follows
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) line[q ^ (lane & 7)] = make_uint4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+                        }
+                        __syncwarp();
+                        const int from = g / width * width, q = lane & 7;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = i * 4 + (lane >> 3);
+                            const uint4 v = reinterpret_cast<const uint4*>(pass)[r * 8 + (q ^ (r & 7))];
+                            const long long at = __shfl_sync(0xffffffffu, to, r);
+                            if (!__shfl_sync(0xffffffffu, (int)mine, r)) continue;
+                            const int at_value = from + q * (width / 8);
+                            if (at_value >= p.dim) continue;
+                            if (whole) *reinterpret_cast<uint4*>(static_cast<E*>(p.out) + at + at_value) = v;
+                            else *reinterpret_cast<uint4*>(p.parts + (part + quarter * 32 + r) * D + at_value) = v;
+                        }
+                        __syncwarp();
+                    }
+                    tmem_fence_before();   // O is read: the next item's products may overwrite it
+                }
+            }
+            ++number;
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+    if (threadIdx.x == 0 && given_up) {   // what this CTA was to leave is not whole
+        p.slots[2 * blockIdx.x].state |= kFailed;
+        p.slots[2 * blockIdx.x + 1].state |= kFailed;
+    }
+}
+
+// ------------------------------------------------------------ joining pieces ---
+
+struct JoinParams {
+    const Slot* slots;
+    const float2* stats;
+    const float* parts;
+    void* out;
+    long long out_stride;
+    int group, dim, tokens, slot_rows;
+    bool causal;
+};
+
+constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+
+// The pieces of the item that CTA blockIdx.x of the attention kernel began and did not end; gridDim.y CTAs
+// share its rows.  A warp takes a row, four values a lane; where an item has many pieces (a few rows, then),
+// the CTA's warps share a row's.
+template <typename E, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams p) {
+    __shared__ float sums[kJoinWarps][D + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Slot head = p.slots[2 * c0 + 1];
+    if (head.state != kFirst) return;
+    // pieces: this one's slot 2 c0 + 1, then slots 2 c of the CTAs after it; one that has none of it is passed over
+    int last = c0;
+    bool whole = true;
+    for (int c = c0 + 1; c < kCtas; ++c) {
+        const Slot s = p.slots[2 * c];
+        if (s.state & kFailed) whole = false;
+        last = c;
+        if ((s.state & kNext) && s.ends) break;
+    }
+    if (!whole) return;   // not stored, like the rest of what a wait that ran out left unfinished
+    const int n = last - c0 + 1;
+    auto slot_of = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
+    const bool shared = n > kJoinWarps;
+    const int first = shared ? blockIdx.y : blockIdx.y * kJoinWarps + warp, step = shared ? gridDim.y : gridDim.y * kJoinWarps;
+    for (int tile = 0; tile < 2; ++tile) {
+        const int tokens = min(p.tokens, head.tokens - tile * p.tokens);
+        for (int row = first; row < tokens * p.group; row += step) {
+            const int token = row / p.group, member = row - token * p.group, at = tile * kRows + row;
+            auto stat = [&](int i) {
+                return i == 0 || p.slots[slot_of(i)].state == kNext ? p.stats[(long long)slot_of(i) * p.slot_rows + at] : make_float2(-INFINITY, 0.0f);
+            };
+            float top = -INFINITY;
+            for (int i = lane; i < n; i += 32) top = fmaxf(top, stat(i).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = shared ? warp : 0; i < n; i += shared ? kJoinWarps : 1) {
+                const float2 s = stat(i);
+                // a piece whose scores are not numbers has a sum that is none; one that saw nothing has no sum
+                if (s.y == 0.0f && s.x == -INFINITY) continue;
+                const float w = s.x == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : power2(s.x - top);
+                l = fmaf(s.y, w, l);
+                if (lane * 4 < D) {
+                    const float4 v = *reinterpret_cast<const float4*>(p.parts + ((long long)slot_of(i) * p.slot_rows + at) * D + lane * 4);
+                    acc[0] = fmaf(v.x, w, acc[0]);
+                    acc[1] = fmaf(v.y, w, acc[1]);
+                    acc[2] = fmaf(v.z, w, acc[2]);
+                    acc[3] = fmaf(v.w, w, acc[3]);
+                }
+            }
+            if (shared) {   // the warps' sums in order
+                __syncthreads();
+                if (lane * 4 < D)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sums[warp][lane * 4 + k] = acc[k];
+                if (lane == 0) sums[warp][D] = l;
+                __syncthreads();
+                if (warp != 0) continue;
+                l = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    l += sums[w][D];
+                    if (lane * 4 < D)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[k] += sums[w][lane * 4 + k];
+                }
+            }
+            Piece c;
+            c.base = head.base;
+            c.keys = head.keys;
+            const int here = tile * p.tokens + token;
+            const bool sees = seen_by(c, p.causal, here) > 0;
+            const float inverse = sees ? 1.0f / l : 0.0f;
+            if (lane * 4 < p.dim) {
+                E* to = static_cast<E*>(p.out) + (long long)(head.q0 + here) * p.out_stride + ((long long)head.head * p.group + member) * p.dim;
+                *reinterpret_cast<uint2*>(to + lane * 4) =
+                    make_uint2(sees ? pack2<E>(acc[0] * inverse, acc[1] * inverse) : 0u, sees ? pack2<E>(acc[2] * inverse, acc[3] * inverse) : 0u);
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host ---
+
+// Heads of a matrix of `rows` rows, boxes of 64 values x `heads_a_box` heads x `rows_a_box` rows.
+int heads_map(CUtensorMap* map, const void* at, int dtype, long long rows, int heads, int dim, long long stride, int heads_a_box,
+              int rows_a_box) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (encode == nullptr) return cuda_failed("cuTensorMapEncodeTiled unavailable", (int)cudaErrorNotSupported);
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)heads_a_box, (cuuint32_t)rows_a_box}, elem[3] = {1, 1, 1};
+    const CUresult r = encode(map, dtype == TR_ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(at), dims, strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_failed("cuTensorMapEncodeTiled", (int)cudaErrorInvalidValue);
+    return TR_OK;
+}
+
+size_t slots_bytes() { return 2 * kCtas * sizeof(Slot); }
+// Rows of a partial result: of both tiles, or where one tile takes all queries, theirs (an even number).
+int slot_rows(long long q_rows, long long group) { return q_rows <= kRows / group ? (int)((q_rows * group + 1) / 2 * 2) : 2 * kRows; }
+size_t stats_bytes(int rows) { return 2 * kCtas * (size_t)rows * sizeof(float2); }
+int padded_dim(long long dim) { return dim <= 64 ? 64 : 128; }
+
+template <typename E, int D>
+int start_tc(TcParams& p, cudaStream_t st) {
+    static std::atomic<bool> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_failed("cudaGetDevice", (int)e);
+    int rc = product_status_word(dev, &p.status);
+    if (rc != TR_OK) return rc;
+    if (!ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(attention_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
+        if (e != cudaSuccess) return cuda_failed("attention kernel set-up", (int)e);
+        ready[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem<D>;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];   // the next kernel may be set up while this one ends
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    rc = launched("attention kernel", (int)cudaLaunchKernelEx(&cfg, attention_kernel<E, D>, p));
+    if (rc != TR_OK) return rc;
+    const JoinParams j{p.slots, p.stats, p.parts, p.out, p.out_stride, p.group, p.dim, p.tokens, p.slot_rows, p.causal};
+    cfg.gridDim = dim3(kCtas, kJoinBlocks);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
+    return launched("attention joining kernel", (int)cudaLaunchKernelEx(&cfg, join_kernel<E, D>, j));
+}
+
+template <typename E>
+int type_tc(TcParams& p, cudaStream_t st) {
+    return p.dim <= 64 ? start_tc<E, 64>(p, st) : start_tc<E, 128>(p, st);
+}
+
+}  // namespace
+
+bool attention_tc_shape(long long heads, long long kv_heads, long long dim) {
+    return dim % 8 == 0 && dim <= 128 && heads / kv_heads <= 64;
+}
+
+bool attention_tc_supported(const AttentionArgs& a) {
+    if (a.dtype == TR_ELEM_F32 || !attention_tc_shape(a.heads, a.kv_heads, a.dim)) return false;
+    if (!(a.scale > 0.0f) || a.scale > 1e30f) return false;
+    auto on16 = [](const void* p, long long stride, long long rows, long long cols) {
+        return (uintptr_t)p % 16 == 0 && (rows <= 1 || (stride % 8 == 0 && stride >= cols && stride < (1LL << 38)));
+    };
+    const long long q_cols = (long long)a.heads * a.dim, k_cols = (long long)a.kv_heads * a.dim;
+    return on16(a.q, a.q_stride, a.q_rows, q_cols) && on16(a.out, a.out_stride, a.q_rows, q_cols) &&
+           (a.k_rows == 0 || (on16(a.k, a.k_stride, a.k_rows, k_cols) && on16(a.v, a.v_stride, a.k_rows, k_cols)));
+}
+
+size_t attention_tc_workspace(long long q_rows, long long heads, long long kv_heads, long long dim) {
+    if (!attention_tc_shape(heads, kv_heads, dim)) return 0;
+    const int rows = slot_rows(q_rows, heads / kv_heads);
+    return slots_bytes() + stats_bytes(rows) + (size_t)2 * kCtas * rows * padded_dim(dim) * sizeof(float);
+}
+
+int launch_attention_tc(const AttentionArgs& a) {
+    TcParams p;
+    p.seq = Sequences{a.q_starts, a.k_starts, a.q_lengths, a.k_lengths, a.q_rows, a.k_rows, a.sequences};
+    p.out = a.out;
+    p.values = a.v;
+    p.out_stride = a.out_stride;
+    p.v_stride = a.v_stride;
+    p.kv_heads = a.kv_heads;
+    p.group = a.heads / a.kv_heads;
+    p.dim = a.dim;
+    p.tokens = kRows / p.group;
+    p.scale = a.scale * 1.44269504088896341f;
+    p.causal = a.causal;
+    uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
+    p.slots = reinterpret_cast<Slot*>(ws);
+    p.stats = reinterpret_cast<float2*>(ws + slots_bytes());
+    p.slot_rows = slot_rows(a.q_rows, p.group);
+    p.parts = reinterpret_cast<float*>(ws + slots_bytes() + stats_bytes(p.slot_rows));
+    p.missing = test_waits();
+    int rc = heads_map(&p.q, a.q, a.dtype, a.q_rows, a.heads, a.dim, a.q_stride, p.group, p.tokens);
+    // (without keys nothing is copied through the other maps)
+    const bool keys = a.k_rows > 0;
+    if (rc == TR_OK)
+        rc = keys ? heads_map(&p.k, a.k, a.dtype, a.k_rows, a.kv_heads, a.dim, a.k_stride, 1, kBoxRows)
+                  : heads_map(&p.k, a.q, a.dtype, 1, a.kv_heads, a.dim, (long long)a.kv_heads * a.dim, 1, kBoxRows);
+    if (rc == TR_OK)
+        rc = keys ? heads_map(&p.v, a.v, a.dtype, a.k_rows, a.kv_heads, a.dim, a.v_stride, 1, kBoxRows)
+                  : heads_map(&p.v, a.q, a.dtype, 1, a.kv_heads, a.dim, (long long)a.kv_heads * a.dim, 1, kBoxRows);
+    if (rc != TR_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+    return a.dtype == TR_ELEM_F16 ? type_tc<__half>(p, st) : type_tc<__nv_bfloat16>(p, st);
+}
+
+}  // namespace trfn
