@@ -4,9 +4,11 @@
 // A CTA on each SM goes through its share of the work (attention_plan.h).  An item
 // is two tiles of 128 rows (queries x heads of one key head) over blocks of 128
 // keys.  Warps: one copies (TMA: queries, then keys and values through a ring of
-// stages) and says what comes next; one issues the products; two make values that
-// a row does not see harmless; four for each tile do the softmax, a thread a row.
-//     S = Q K^T into TMEM; a row's thread reads it, keeps maximum and sum, writes
+// stages) and says what comes next; one issues the products; one makes values that
+// a row does not see harmless; eight for each tile do the softmax, two threads a row
+// (64 scores are what a thread can hold, and four warps to a scheduler hide one
+// another's waits: 128 scores in one thread of four warps took twice as long).
+//     S = Q K^T into TMEM; a row's threads read it, keep maximum and sum, writes
 //     P = 2^(x - m) in 16 bits over S; O += P V in TMEM, P read from there.
 // The tiles take turns: the tensor cores multiply for one while the other's
 // weights are made.  O is multiplied by 2^(m_old - m_new) only where the maximum
@@ -33,8 +35,10 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "attention_parts.h"
+#include "f32_pairs.h"
 #include "tensor_core.h"
 
 namespace trfn {
@@ -45,7 +49,7 @@ using attention::kKeys;
 using attention::kRows;
 
 constexpr int kCtas = 152;                    // one on each SM
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8, kThreads = 32 * (4 + kSoftmaxWarps);
 constexpr int kPieces = 8, kFlags = 16;       // descriptors on their way; items whose values may be under way
 constexpr int kBoxRows = 64;                  // keys to a copy
 constexpr float kGrowth = 8.0f;               // of a maximum, in powers of two, before O is multiplied
@@ -57,9 +61,11 @@ struct Piece {
     int k0, keys;        // the sequence's first key's row, and keys
     int base;            // keys that its first query sees (before the bounds); causal: one more for each query
     int j0, j1;          // blocks of this piece; j0 < 0: nothing follows
-    int n0, n1;          // blocks that the tiles' rows see
     int slot;            // partial result, or -1
-    int pad[5];
+    int end0, end1;      // where the tiles' blocks end, up to j1
+    int least;           // keys that its first query sees
+    int seen0, seen1;    // keys that the tiles' last queries see
+    int pad[2];
 };
 static_assert(sizeof(Piece) == 64, "pieces of the workspace and of shared memory");
 
@@ -96,17 +102,58 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(c), "r"(head), "r"(row), "r"(bar)
         : "memory");
 }
-// Issued by the whole warp for its one elected thread.
-__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
+// Four products, 64 values of K, issued by the whole warp for its one elected thread: as one piece of PTX, whose
+// operands are made once (four pieces, each with an election and operands of its own, kept the tensor cores waiting
+// where other warps were busy: 145 cycles a product for 64).
+__device__ __forceinline__ void mma4_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"(add)
+        "{\n"
+        "\t.reg .pred p, e, t;\n"
+        "\t.reg .b64 a, b;\n"
+        "\telect.sync _|e, 0xffffffff;\n"
+        "\tsetp.ne.b32 p, %4, 0;\n"
+        "\tsetp.eq.b32 t, 0, 0;\n"
+        "\tadd.s64 a, %1, 0;\n"
+        "\tadd.s64 b, %2, 0;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        "\tadd.s64 a, %1, 2;\n"
+        "\tadd.s64 b, %2, 2;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "\tadd.s64 a, %1, 4;\n"
+        "\tadd.s64 b, %2, 4;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "\tadd.s64 a, %1, 6;\n"
+        "\tadd.s64 b, %2, 6;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "}\n"::"r"(d), "l"(a), "l"(b), "r"(shape), "r"(add)
         : "memory");
 }
-// A in TMEM, two 16-bit values to a column.
+// A in TMEM, two 16-bit values to a column; B's rows along K, 2 KB to 16 of them.
+__device__ __forceinline__ void mma4_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, uint32_t add) {
+    asm volatile(
+        "{\n"
+        "\t.reg .pred p, e, t;\n"
+        "\t.reg .b64 b;\n"
+        "\t.reg .b32 a;\n"
+        "\telect.sync _|e, 0xffffffff;\n"
+        "\tsetp.ne.b32 p, %4, 0;\n"
+        "\tsetp.eq.b32 t, 0, 0;\n"
+        "\tadd.s32 a, %1, 0;\n"
+        "\tadd.s64 b, %2, 0;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n"
+        "\tadd.s32 a, %1, 8;\n"
+        "\tadd.s64 b, %2, 128;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "\tadd.s32 a, %1, 16;\n"
+        "\tadd.s64 b, %2, 256;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "\tadd.s32 a, %1, 24;\n"
+        "\tadd.s64 b, %2, 384;\n"
+        "\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "}\n"::"r"(d), "r"(a), "l"(b), "r"(shape), "r"(add)
+        : "memory");
+}
+// One such product.
 __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, uint32_t add) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\t"
@@ -140,16 +187,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
           "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
           "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
-}
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
-        "r"(v[31])
-        : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
     asm volatile(
@@ -187,6 +224,28 @@ template <> __device__ __forceinline__ uint32_t not_finite2<__nv_bfloat16>(uint3
 __device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
 __device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+template <typename E> __device__ __forceinline__ E from_value(float v);
+template <> __device__ __forceinline__ __half from_value<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_value<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// bar_wait (tensor_core.h) without its call: what a call keeps in local memory would be fetched from L2 after every
+// wait, as shared memory leaves no room for it in L1.
+__device__ __forceinline__ bool bar_wait_here(uint32_t bar, uint32_t parity, volatile int* given_up, unsigned* status) {
+    if (bar_try(bar, parity)) return true;
+    uint32_t t0 = 0;
+    for (uint32_t i = 1; i < (1u << 28); ++i) {
+        if (bar_try(bar, parity)) return true;
+        if ((i & 255u) != 0) continue;
+        if (*given_up) return false;
+        const uint32_t now = (uint32_t)(now_ns() >> 10);   // about microseconds
+        if (t0 == 0) t0 = now | 1u;
+        else if (now - t0 > (uint32_t)(kWaitLimitNs >> 10)) break;
+    }
+    *given_up = 1;
+    atomicOr(status, kStatusTimeout);
+    return false;
+}
+
 // The exponent of the type is all ones: one value.
 template <typename E> constexpr uint32_t kExponent = 0x7c00;
 template <> constexpr uint32_t kExponent<__nv_bfloat16> = 0x7f80;
@@ -196,19 +255,20 @@ template <> constexpr float kLift<__nv_bfloat16> = 0.0f;
 
 // ------------------------------------------------------------- the layout ---
 
-// Shared memory, D = 64 or 128: queries of two tiles (kQ of them), the ring, 4 KB for each softmax warp.
+// Shared memory, D = 64 or 128: queries of two tiles (kQ of them), the ring, 1 KB for each softmax warp.
 template <int D> constexpr int kTileBytes = kRows * D * 2;    // of queries, of a block of keys or values
 template <int D> constexpr int kQ = D == 64 ? 2 : 1;
 template <int D> constexpr int kStages = D == 64 ? 7 : 4;
-template <int D> constexpr int kSmem = 1024 + kQ<D> * 2 * kTileBytes<D> + kStages<D> * kTileBytes<D> + 8 * 4096;
+template <int D> constexpr int kSmem = 1024 + kQ<D> * 2 * kTileBytes<D> + kStages<D> * kTileBytes<D> + kSoftmaxWarps * 1024;
 
 __device__ __forceinline__ int seen_by(const Piece& p, bool causal, int token) {
     if (!causal) return p.keys;
     const long long n = (long long)p.base + token;
     return (int)max(0LL, min(n, (long long)p.keys));
 }
-// Whether some row does not see the whole of block j.
-__device__ __forceinline__ bool masked(const Piece& p, bool causal, int j) { return (long long)(j + 1) * kKeys > seen_by(p, causal, 0); }
+// Whether some row of an item, whose first query sees `least` keys, does not see the whole of block j.
+__device__ __forceinline__ bool masked(int least, int j) { return (least >> 7) <= j; }
+static_assert(kKeys == 128, "blocks are counted by a shift");
 
 __device__ __forceinline__ attention::Sequence sequence_of(const TcParams& p, int s) {
     return attention::Sequence{range_of(p.seq.q_starts, p.seq.q_lengths, s, p.seq.q_rows).length,
@@ -300,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int s = 0; s < ST; ++s) {
             bar_init(full(s), s == 0 && blockIdx.x == 0 ? 1 + p.missing : 1);
             bar_init(empty(s), 1);
-            bar_init(clean(s), 2);
+            bar_init(clean(s), 1);
         }
         for (int s = 0; s < NQ; ++s) {
             bar_init(q_full(s), 1);
@@ -308,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         for (int s = 0; s < kPieces; ++s) {
             bar_init(piece_full(s), 1);
-            bar_init(piece_empty(s), 11);   // the products' warp, two that clean, eight softmax warps
+            bar_init(piece_empty(s), 2 + kSoftmaxWarps);   // the products' warp, the one that cleans, the softmax
         }
         for (int t = 0; t < 2; ++t) {
             bar_init(scores(t), 1);
-            bar_init(weights(t), 4);
+            bar_init(weights(t), kSoftmaxWarps / 2);
             bar_init(summed(t), 1);
         }
         for (int i = 0; i < kFlags; ++i) not_finite[i] = -1;
@@ -329,16 +389,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t tmem = tmem_at;
     auto s_at = [&](int t) { return tmem + t * kKeys; };
     auto o_at = [&](int t) { return tmem + 2 * kKeys + t * D; };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, &given_up, p.status); };
-    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, &given_up, p.status)) != 0; };
-    // The piece with this number, once it is there; the warp is done with its place then.
-    auto next_piece = [&](int number, Piece& to) {
-        const int s = number % kPieces;
-        if (!wait_all(piece_full(s), (number / kPieces) & 1)) return false;
-        to = pieces[s];
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait_here(bar, parity, &given_up, p.status); };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait_here(bar, parity, &given_up, p.status)) != 0; };
+    // Whether the piece with this number is there and not the end; and that the warp is done with it.
+    auto next_piece = [&](int number) {
+        return wait_all(piece_full(number % kPieces), (number / kPieces) & 1) && pieces[number % kPieces].j0 >= 0;
+    };
+    auto piece_done = [&](int number) {
         __syncwarp();
-        if (lane == 0) arrive(piece_empty(s));
-        return to.j0 >= 0;
+        if (lane == 0) arrive(piece_empty(number % kPieces));
     };
 
     if (warp == 0) {
@@ -346,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             Border b = borders[0];
             long long left = borders[1].unit - b.unit;
             // nothing of an earlier call is left in the slots
-            Slot slot[2] = {};
+            Slot* const slots = p.slots + 2 * blockIdx.x;
+            slots[0].state = slots[1].state = 0;
             int number = 0, item = 0;   // pieces, and those with blocks
             int s = 0, issued = 0;
             uint32_t phase = 0;
@@ -380,15 +440,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     c.k0 = rk.start;
                     c.keys = rk.length;
                     c.base = (int)((long long)i0 + 1 + rk.length - rq.length);
-                    c.n0 = step.n0;
-                    c.n1 = step.n1;
                     c.j0 = step.j0;
                     c.j1 = step.j1;
+                    c.end0 = min(step.j1, step.n0);
+                    c.end1 = min(step.j1, step.n1);
+                    c.least = seen_by(c, p.causal, 0);
+                    c.seen0 = seen_by(c, p.causal, min(c.tokens, p.tokens) - 1);
+                    c.seen1 = seen_by(c, p.causal, c.tokens - 1);
                     c.slot = -1;
                     if (!step.begins || !step.ends) {
                         const int which = step.begins ? 1 : 0;
                         c.slot = 2 * blockIdx.x + which;
-                        slot[which] = Slot{step.begins ? kFirst : kNext, step.ends, c.q0, c.tokens, c.head, c.keys, c.base, 0};
+                        slots[which] = Slot{step.begins ? kFirst : kNext, step.ends, c.q0, c.tokens, c.head, c.keys, c.base, 0};
                     }
                     ok = wait(piece_empty(number % kPieces), ((number / kPieces) & 1) ^ 1u);
                     if (!ok) break;
@@ -419,8 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 pieces[number % kPieces].j0 = -1;
                 arrive(piece_full(number % kPieces));
             }
-            p.slots[2 * blockIdx.x] = slot[0];
-            p.slots[2 * blockIdx.x + 1] = slot[1];
             // copies in flight land before the CTA ends, whatever became of the others
             for (int i = 0; i < issued; ++i) {
                 s = s == 0 ? ST - 1 : s - 1;
@@ -431,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
     } else if (warp == 1) {
         int s = 0, number = 0, item = 0;
-        uint32_t phase = 0, weights_phase[2] = {0, 0};
+        uint32_t phase = 0, weights_phase0 = 0, weights_phase1 = 0;
         uint32_t last = 0, last_phase = 0;   // the stage whose products were issued last
         auto advance = [&] {
             commit(empty(s));
@@ -439,108 +500,136 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             last_phase = phase;
             if (++s == ST) { s = 0; phase ^= 1u; }
         };
-        // the next piece that has blocks
-        auto with_blocks = [&](Piece& to) {
+        // What the products need to know of a piece, in registers that the compiler knows to be the same in every
+        // lane (a maximum over the warp is): operands of other registers cost each product a loop over lanes.
+        auto same = [](int v) { return __reduce_max_sync(0xffffffffu, v); };
+        const uint32_t tm = (uint32_t)same((int)tmem), queries_u = (uint32_t)same((int)queries), ring_u = (uint32_t)same((int)ring);
+        int j0 = 0, j1 = 0, end0 = 0, end1 = 0, seen0 = 0, seen1 = 0;               // the piece whose P V come next
+        int next_j0 = 0, next_j1 = 0, next_end0 = 0, next_end1 = 0, next_seen0 = 0, next_seen1 = 0;   // the one after it
+        // that one: the next that has blocks
+        auto look_ahead = [&] {
             do {
-                if (!next_piece(number, to)) return false;
+                const int at = number % kPieces;
+                if (!wait_all(piece_full(at), (number / kPieces) & 1)) return false;
+                const Piece& c = pieces[at];
+                next_j0 = same(c.j0);
+                next_j1 = same(c.j1);
+                next_end0 = same(c.end0);
+                next_end1 = same(c.end1);
+                next_seen0 = same(c.seen0);
+                next_seen1 = same(c.seen1);
+                __syncwarp();
+                if (lane == 0) arrive(piece_empty(at));
+                if (next_j0 < 0) return false;
                 ++number;
-            } while (to.j1 <= to.j0);
+            } while (next_j1 <= next_j0);
             return true;
         };
-        const uint32_t n_values = (uint32_t)(p.dim + 15) / 16, k_steps = n_values;
-        auto end_of = [](const Piece& c, int t) { return min(c.j1, t == 0 ? c.n0 : c.n1); };
-        // keys of block j that some row of tile t sees
-        auto columns = [&](const Piece& c, int t, int j) {
-            const int token = min(c.tokens, (t + 1) * p.tokens) - 1;
-            return min(kKeys, seen_by(c, p.causal, token) - j * kKeys);
+        auto go_on = [&] {
+            j0 = next_j0;
+            j1 = next_j1;
+            end0 = next_end0;
+            end1 = next_end1;
+            seen0 = next_seen0;
+            seen1 = next_seen1;
         };
-        auto score = [&](const Piece& c, int t, int j, int qs, int stage) {
-            const uint64_t a = operand(queries + (qs * 2 + t) * kTileBytes<D>), b = operand(ring + stage * kTileBytes<D>);
-            const uint32_t n = (uint32_t)(columns(c, t, j) + 15) / 16;
-            for (uint32_t k = 0; k < k_steps; ++k) {
-                const uint32_t at = (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2;   // 64 values lie 16 KB from the next
-                mma_shared(s_at(t), a + at, b + at, kShape | (2 * n << 17), k > 0);
-            }
+        const int n_values = (p.dim + 15) / 16;
+        // S of tile t for block j, of whose keys some row of the tile sees seen - 128 j
+        auto score = [&](int t, int seen, int j, int qs, int stage) {
+            const uint64_t a = operand(queries_u + (uint32_t)same((qs * 2 + t) * kTileBytes<D>));
+            const uint64_t b = operand(ring_u + (uint32_t)same(stage * kTileBytes<D>));
+            const uint32_t shape = kShape | (uint32_t)same((min(kKeys, seen - j * kKeys) + 15) / 16 << 18);
+            // (all of D: what a shorter head lacks was copied as zeros)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)   // 64 values lie 16 KB from the next
+                mma4_shared(tm + t * kKeys, a + k * (kRows * 128 / 16), b + k * (kRows * 128 / 16), shape, k > 0);
             commit(scores(t));
         };
-        auto weigh = [&](const Piece& c, int t, int j, int stage) {
-            const uint64_t b = operand_across(ring + stage * kTileBytes<D>, kKeys * 128);
-            const int steps = (columns(c, t, j) + 15) / 16;
-            for (int k = 0; k < steps; ++k)
-                mma_tmem(o_at(t), s_at(t) + k * 8, b + k * (16 * 128 / 16), kShape | (1u << 16) | (2 * n_values << 17), j > c.j0 || k > 0);
+        auto weigh = [&](int t, int seen, int j, int stage, bool add) {
+            const uint64_t b = operand_across(ring_u + (uint32_t)same(stage * kTileBytes<D>), kKeys * 128);
+            const int steps = same((min(kKeys, seen - j * kKeys) + 15) / 16);
+            const uint32_t shape = kShape | (1u << 16) | (uint32_t)(n_values << 18), more = (uint32_t)same(add);
+            const uint32_t o = tm + 2 * kKeys + t * D, w = tm + t * kKeys;
+            if (steps == kKeys / 16) {
+                mma4_tmem(o, w, b, shape, more);
+                mma4_tmem(o, w + 32, b + 4 * 128, shape, 1);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) mma_tmem(o, w + k * 8, b + k * 128, shape, k > 0 ? 1u : more);
+            }
             commit(summed(t));
         };
-        Piece cur, nxt;
-        bool ok = with_blocks(cur);
+        bool ok = look_ahead();
         if (ok) {
+            go_on();
             ok = wait_all(q_full(0), 0) && wait_all(full(s), phase);
             if (ok) {
                 tmem_fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (cur.j0 < end_of(cur, t)) score(cur, t, cur.j0, 0, s);
+                if (j0 < end0) score(0, seen0, j0, 0, s);
+                if (j0 < end1) score(1, seen1, j0, 0, s);
                 advance();
-                if (cur.j0 + 1 == cur.j1) commit(q_empty(0));
+                if (j0 + 1 == j1) commit(q_empty(0));
             }
         }
         while (ok) {
             bool more = false;
-            for (int j = cur.j0; j < cur.j1 && ok; ++j) {
+            for (int j = j0; j < j1 && ok; ++j) {
                 const int v_stage = s;
                 ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
                 if (!ok) break;
                 // the block whose scores come next: this piece's, or the first of the next one
-                const bool inside = j + 1 < cur.j1;
-                more = inside || with_blocks(nxt);
-                const Piece& then = inside ? cur : nxt;
-                const int then_j = inside ? j + 1 : nxt.j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
+                const bool inside = j + 1 < j1;
+                more = inside || look_ahead();
+                const int then_j = inside ? j + 1 : next_j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
+                const int then_end0 = inside ? end0 : next_end0, then_end1 = inside ? end1 : next_end1;
                 const int k_stage = s + 1 == ST ? 0 : s + 1;
                 const uint32_t k_phase = s + 1 == ST ? phase ^ 1u : phase;
-                bool there = false;
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j < end_of(cur, t)) {
-                        ok = wait_all(weights(t), weights_phase[t]);
-                        weights_phase[t] ^= 1u;
-                        if (!ok) break;
-                        tmem_fence_after();
-                        weigh(cur, t, j, v_stage);
-                    }
-                    if (more && then_j < end_of(then, t)) {
-                        if (!there) {
-                            ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
-                            if (!ok) break;
-                            tmem_fence_after();
-                            there = true;
-                        }
-                        score(then, t, then_j, qs, k_stage);
-                    }
+                if (j < end0) {
+                    ok = wait_all(weights(0), weights_phase0);
+                    weights_phase0 ^= 1u;
+                    if (!ok) break;
+                    tmem_fence_after();
+                    weigh(0, seen0, j, v_stage, j > j0);
                 }
-                if (!ok) break;
+                if (more) {
+                    ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (then_j < then_end0) score(0, inside ? seen0 : next_seen0, then_j, qs, k_stage);
+                }
+                if (j < end1) {
+                    ok = wait_all(weights(1), weights_phase1);
+                    weights_phase1 ^= 1u;
+                    if (!ok) break;
+                    tmem_fence_after();
+                    weigh(1, seen1, j, v_stage, j > j0);
+                }
+                if (more && then_j < then_end1) score(1, inside ? seen1 : next_seen1, then_j, qs, k_stage);
                 advance();
                 if (more) {
                     advance();
-                    if (then_j + 1 == then.j1) commit(q_empty(qs));
+                    if (then_j + 1 == (inside ? j1 : next_j1)) commit(q_empty(qs));
                 }
             }
             if (!more) break;
-            cur = nxt;
+            go_on();
             ++item;
         }
         if (last != 0) bar_drain(last, last_phase);   // the last products are done before TMEM is freed
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // Values that a row does not see: rows of the ring beyond the keys become zeros, values that are not finite too.
-        // (The products wait for these warps at every block of values, so neither is ever a turn of the ring ahead.)
-        const int me = threadIdx.x - 64;
+        // (The products wait for this warp at every block of values, so it is never a turn of the ring ahead.)
         int s = 0, number = 0;
         uint32_t phase = 0;
-        Piece c;
         bool ok = true;
         auto done = [&] {
             __syncwarp();
             if (lane == 0) arrive(clean(s));
             if (++s == ST) { s = 0; phase ^= 1u; }
         };
-        while (ok && next_piece(number, c)) {
+        while (ok && next_piece(number)) {
+            const Piece& c = pieces[number % kPieces];
             bool found = false;
             for (int j = c.j0; j < c.j1 && ok; ++j) {
                 ok = wait_all(full(s), phase);   // keys
@@ -548,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 done();
                 ok = wait_all(full(s), phase);
                 if (!ok) break;
-                if (masked(c, p.causal, j)) {
+                if (masked(c.least, j)) {
                     uint8_t* const at = base + NQ * 2 * kTileBytes<D> + s * kTileBytes<D>;
                     const int rows = min(kKeys, c.keys - j * kKeys), whole = (rows + 15) / 16 * 16;
                     bool wrote = false;
                     for (int col = 0; col < COLS; ++col)
-                        for (int i = me; i < whole * 8; i += 64) {   // 16 bytes
+                        for (int i = lane; i < whole * 8; i += 32) {   // 16 bytes
                             uint4* const v = reinterpret_cast<uint4*>(at + col * (kKeys * 128)) + i;
                             if (i >= rows * 8) {
                                 *v = make_uint4(0, 0, 0, 0);
@@ -571,48 +660,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             *v = make_uint4(w[0], w[1], w[2], w[3]);
                             wrote = found = true;
                         }
-                    if (found) not_finite[number % kFlags] = number;
+                    if (__any_sync(0xffffffffu, found) && lane == 0) not_finite[number % kFlags] = number;
                     if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 done();
             }
-            ++number;
+            if (!ok) break;
+            piece_done(number++);
         }
-    } else {
+    } else if (warp >= 4) {
         const int tile = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        uint8_t* const pass = passes + (warp - 4) * 4096;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16, s_mine = s_at(tile) + lanes, o_mine = o_at(tile) + lanes;
-        const int token = row / p.group, member = row - token * p.group;
-        uint32_t scores_phase = 0, products = 0;   // products of P and V so far
+        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int token = row / p.group;
+        uint32_t products = 0;   // scores seen and products of P and V asked for, so far
         int number = 0;
-        Piece c;
         bool ok = true;
-        while (ok && next_piece(number, c)) {
+        while (ok && next_piece(number)) {
+            const Piece& c = pieces[number % kPieces];
             const int here = tile * p.tokens + token;   // of the item's queries
             const bool mine = token < p.tokens && here < c.tokens;
-            const bool some = __any_sync(0xffffffffu, mine), tile_has = c.tokens > tile * p.tokens;
+            const bool some = __any_sync(0xffffffffu, mine);
             const int seen = mine ? seen_by(c, p.causal, here) : 0;
-            const int last_seen = seen_by(c, p.causal, min(c.tokens, (tile + 1) * p.tokens) - 1);
-            const int e = min(c.j1, tile == 0 ? c.n0 : c.n1);
-            float ms = -INFINITY, l = 0.0f;   // the maximum times the scale, less the lift
-            for (int j = c.j0; j < e; ++j) {
-                ok = wait_all(scores(tile), scores_phase);
-                scores_phase ^= 1u;
+            const int last_seen = tile == 0 ? c.seen0 : c.seen1;
+            const int e = tile == 0 ? c.end0 : c.end1, begin = c.j0, least = c.least;
+            float ms = -INFINITY, l = 0.0f;   // the maximum times the scale, less the lift; the sum of the weights
+            for (int j = begin; j < e; ++j) {
+                ok = wait_all(scores(tile), products & 1);
                 if (!ok) break;
                 tmem_fence_after();
                 if (some) {
                     const int cols = min(kKeys, last_seen - j * kKeys);   // of the tile
                     uint32_t x[kKeys];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (g * 32 < cols) tmem_load32(s_mine + g * 32, x + g * 32);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i) asm volatile("" : "+r"(x[i]));
-                    if (masked(c, p.causal, j)) {
+                    tmem_load32(tm + tile * kKeys, x);
+                    tmem_load32(tm + tile * kKeys + 32, x + 32);
+                    tmem_load32(tm + tile * kKeys + 64, x + 64);
+                    tmem_load32(tm + tile * kKeys + 96, x + 96);
+                    tmem_wait(x);
+                    if (masked(least, j)) {
                         const int sees = seen - j * kKeys;
 #pragma unroll
-                        for (int i = 0; i < kKeys; ++i) x[i] = i < sees ? x[i] : 0xff800000u;
+                        for (int i = 0; i < kKeys; ++i)
+                            if (i >= sees) x[i] = 0xff800000u;
                     }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -628,38 +716,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             ms = high;
                             l *= factor;
                         }
-                        if (j > c.j0) {
+                        if (j > begin) {
                             ok = wait_all(summed(tile), (products - 1) & 1);
                             if (!ok) break;
                             tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int g = 0; g < D; g += 16) {
                                 uint32_t o[16];
-                                tmem_load16(o_mine + g, o);
+                                tmem_load16(tm + 2 * kKeys + tile * D + g, o);
                                 tmem_wait(o);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                                tmem_store16(o_mine + g, o);
+                                tmem_store16(tm + 2 * kKeys + tile * D + g, o);
                             }
                         }
                     }
                     const float off = ms == -INFINITY ? 0.0f : ms;   // nothing seen yet: weights 0
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const Two scale2 = two(p.scale, p.scale), off2 = two(-off, -off);
+                    Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (g * 64 >= cols) continue;
-                        uint32_t w[32];
+                    for (int g = 0; g < 4; ++g) {
+                        if (g * 32 >= cols) continue;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) {
-                            const float a = power2(fmaf(__uint_as_float(x[g * 64 + i]), p.scale, -off));
-                            const float b = power2(fmaf(__uint_as_float(x[g * 64 + i + 1]), p.scale, -off));
-                            sum[i & 2] += a;
-                            sum[(i & 2) + 1] += b;
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y = apart(fma_two(two(__uint_as_float(x[g * 32 + i]), __uint_as_float(x[g * 32 + i + 1])), scale2, off2));
+                            const float a = power2(y.x), b = power2(y.y);
+                            sum[i / 2 & 1] = add_two(sum[i / 2 & 1], two(a, b));
                             w[i / 2] = pack2<E>(a, b);
                         }
-                        tmem_store32(s_mine + g * 32, w);
+                        tmem_store16(tm + tile * kKeys + g * 16, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 all = apart(add_two(sum[0], sum[1]));
+                    l += all.x + all.y;
                     tmem_stored();
                 }
                 tmem_fence_before();
@@ -668,78 +757,88 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 ++products;
             }
             if (!ok) break;
-            if (tile_has && some) {
-                const bool any = e > c.j0;
+            if (some) {
+                const bool any = e > begin;
                 if (any) {
                     ok = wait_all(summed(tile), (products - 1) & 1);
                     if (!ok) break;
                     tmem_fence_after();
                 }
-                const bool repair = any && not_finite[number % kFlags] == number;
+                // what only this end of a piece needs is made here, not kept in registers meanwhile
+                int me = threadIdx.x - 128;
+                asm volatile("" : "+r"(me));
+                uint8_t* const pass = passes + (me >> 5) * 1024;
+                const int member = (me & 127) - token * p.group;
                 const bool whole = c.slot < 0;
-                const long long part = (long long)max(c.slot, 0) * p.slot_rows + tile * kRows;
-                if (!whole && mine) p.stats[part + row] = make_float2(any ? ms : -INFINITY, any ? l : 0.0f);
-                const float inverse = !whole ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
-                // where this row goes, for the lanes that write it
-                const long long to = (long long)(c.q0 + here) * p.out_stride + ((long long)c.head * p.group + member) * p.dim;
+                const int part_row = max(c.slot, 0) * p.slot_rows + tile * kRows + row;
+                if (!whole && mine) p.stats[part_row] = make_float2(any ? ms : -INFINITY, any ? l : 0.0f);
+                const float inverse = !any || seen == 0 ? 0.0f : whole ? 1.0f / l : 1.0f;
+                // where this row goes, for the lanes that write it; rows of nothing go nowhere
+                const char* const to = !mine           ? nullptr
+                                       : whole ? static_cast<const char*>(p.out) + ((long long)(c.q0 + here) * p.out_stride +
+                                                                                     ((long long)c.head * p.group + member) * p.dim) * 2
+                                               : reinterpret_cast<const char*>(p.parts + (long long)part_row * D);
+                const int until = p.dim;
+                const int at_lane = me & 31;
+                uint4* const line = reinterpret_cast<uint4*>(pass) + at_lane * 2;
+                const uint4* const from = reinterpret_cast<const uint4*>(pass) + (at_lane >> 1) * 2 + ((at_lane & 1) ^ (at_lane >> 3 & 1));
                 if (whole || any) {
-                    const int width = whole ? 64 : 32;   // values of 128 bytes
-                    for (int g = 0; g < p.dim; g += 32) {
-                        uint32_t o[32];
-                        if (any) {
-                            tmem_load32(o_mine + g, o);
-                            tmem_wait(o);
-                        }
+#pragma unroll 1
+                    for (int g = 0; g < until; g += 8) {
+                        uint32_t o[8];
+                        tmem_load(tm + 2 * kKeys + tile * D + g, o);
+                        tmem_wait(o);
+                        // (a row that sees nothing gets zeros, whatever its sums are)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = any && seen > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
-                        if (repair && mine) {
-                            // values of masked blocks that are not finite, for the rows that see them
-                            const int from = max(c.j0, seen_by(c, p.causal, 0) / kKeys) * kKeys, until = min(seen, e * kKeys);
-                            for (int k = from; k < until; ++k) {
-                                const E* v = static_cast<const E*>(p.values) + (long long)(c.k0 + k) * p.v_stride + (long long)c.head * p.dim + g;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (g + i < p.dim) {
-                                        const float f = value_of(v[i]);
-                                        if (!isfinite(f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
-                                    }
-                            }
-                        }
-                        // through the warp's 4 KB, so that rows are written in runs of 128 bytes; 16-byte piece q of
-                        // row r lies at q ^ (r & 7): no bank conflicts
-                        uint4* const line = reinterpret_cast<uint4*>(pass) + lane * 8;
+                        for (int i = 0; i < 8; ++i) o[i] = inverse == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inverse);
+                        // through the warp's 1 KB, so that rows are written in runs of 32 bytes; 16-byte piece q of
+                        // row r lies at q ^ (r >> 2 & 1): no bank conflicts
+                        const int turned = lane >> 2 & 1;
                         if (whole) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                line[((g / 8 & 4) + q) ^ (lane & 7)] =
-                                    make_uint4(pack2<E>(__uint_as_float(o[q * 8]), __uint_as_float(o[q * 8 + 1])),
-                                               pack2<E>(__uint_as_float(o[q * 8 + 2]), __uint_as_float(o[q * 8 + 3])),
-                                               pack2<E>(__uint_as_float(o[q * 8 + 4]), __uint_as_float(o[q * 8 + 5])),
-                                               pack2<E>(__uint_as_float(o[q * 8 + 6]), __uint_as_float(o[q * 8 + 7])));
-                            if (g % 64 == 0 && g + 32 < p.dim) continue;   // the line's other half follows
+                            line[(g >> 3 & 1) ^ turned] = make_uint4(pack2<E>(__uint_as_float(o[0]), __uint_as_float(o[1])),
+                                                                     pack2<E>(__uint_as_float(o[2]), __uint_as_float(o[3])),
+                                                                     pack2<E>(__uint_as_float(o[4]), __uint_as_float(o[5])),
+                                                                     pack2<E>(__uint_as_float(o[6]), __uint_as_float(o[7])));
+                            if ((g & 8) == 0 && g + 8 < until) continue;   // the line's other half follows
                         } else {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) line[q ^ (lane & 7)] = make_uint4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+                            line[turned] = make_uint4(o[0], o[1], o[2], o[3]);
+                            line[turned ^ 1] = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         __syncwarp();
-                        const int from = g / width * width, q = lane & 7;
+                        const int at = whole ? ((g & ~8) + (lane & 1) * 8) * 2 : (g + (lane & 1) * 4) * 4;
+                        const bool in = !whole || (g & ~8) + (lane & 1) * 8 < until;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = i * 4 + (lane >> 3);
-                            const uint4 v = reinterpret_cast<const uint4*>(pass)[r * 8 + (q ^ (r & 7))];
-                            const long long at = __shfl_sync(0xffffffffu, to, r);
-                            if (!__shfl_sync(0xffffffffu, (int)mine, r)) continue;
-                            const int at_value = from + q * (width / 8);
-                            if (at_value >= p.dim) continue;
-                            if (whole) *reinterpret_cast<uint4*>(static_cast<E*>(p.out) + at + at_value) = v;
-                            else *reinterpret_cast<uint4*>(p.parts + (part + quarter * 32 + r) * D + at_value) = v;
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 v = from[i * 32];
+                            const char* const row_to = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, (unsigned long long)to, i * 16 + (lane >> 1)));
+                            if (in && row_to != nullptr) *reinterpret_cast<uint4*>(const_cast<char*>(row_to) + at) = v;
                         }
                         __syncwarp();
                     }
                     tmem_fence_before();   // O is read: the next item's products may overwrite it
                 }
+                if (any && not_finite[number % kFlags] == number && mine) {
+                    // values of masked blocks that are not finite, for the rows that see them: added to what was written
+                    const int first = max(begin, least / kKeys) * kKeys, end = min(seen, e * kKeys);
+                    char* const out = const_cast<char*>(to);
+#pragma unroll 1
+                    for (int k = first; k < end; ++k) {
+                        const E* const v = static_cast<const E*>(p.values) + (long long)(c.k0 + k) * p.v_stride + (long long)c.head * p.dim;
+#pragma unroll 1
+                        for (int d = 0; d < until; ++d) {
+                            const float f = value_of(v[d]);
+                            if (isfinite(f)) continue;
+                            if (whole) {
+                                E* const o = reinterpret_cast<E*>(out) + d;
+                                *o = from_value<E>(value_of(*o) + f);
+                            } else {
+                                reinterpret_cast<float*>(out)[d] += f;
+                            }
+                        }
+                    }
+                }
             }
-            ++number;
+            piece_done(number++);
         }
     }
     __syncthreads();

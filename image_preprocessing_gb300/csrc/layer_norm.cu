@@ -214,12 +214,6 @@ struct LayerGradParams {
     float eps;
 };
 
-__device__ __forceinline__ Two add_two(Two a, Two b) {
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Rows that a CTA takes at a time, and the packs of the next rows that its
 // threads copy into shared memory meanwhile, as in the RMS norm's gradient.
 template <int V, int T, int NV> constexpr int kLayerRowBytes = V > 1 ? 3 * NV * 16 * kThreads<T> : 0;

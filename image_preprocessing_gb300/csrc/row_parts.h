@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "f32_pairs.h"
 #include "token_ops.h"
 
 namespace trfn {
@@ -188,29 +189,6 @@ int launch_row_kernel(const char* what, void (*kernel)(P...), unsigned grid, uns
 template <int T> constexpr int kThreads = T <= 32 ? 256 : T;
 
 __host__ __device__ constexpr int padded(int c) { return c + (c >> 5); }
-
-// Two binary32 values in one register pair, and the instructions that work on both.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float a, float b) {
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 apart(Two v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ Two mul_two(Two a, Two b) {
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // How the rows of a matrix lie on packs of V values of es bytes: 0 all of them
 // on boundaries, f > 0 row r starts f r mod V values into a pack, -1 neither.
