@@ -38,7 +38,8 @@ int main() {
                 seen = seen < 0 ? 0 : seen > q.lk ? q.lk : seen;
                 const long long blocks = (seen + kKeys - 1) / kKeys;
                 if (blocks != q.item_blocks(t)) fail("item_blocks", blocks, q.item_blocks(t));
-                w += blocks > 0 ? blocks : 1;
+                w += blocks + kItemCost;
+                if (w != q.units_before(t + 1)) fail("units_before", w, q.units_before(t + 1));
             }
             if (w != q.head_units()) fail("head_units", w, q.head_units());
             units += w * kv_heads;
@@ -75,6 +76,7 @@ int main() {
                     if (t.head != at_head || t.item != at_item || t.j0 != at_block) fail("place", t.item, at_item);
                     if (t.begins != (at_block == 0)) fail("begins", t.j0, at_block);
                     const int blocks = seq[at_s].item_blocks(at_item);
+                    if (before - left > t.j1 - t.j0 + (t.begins ? kItemCost : 0)) fail("units and blocks", before - left, t.j1 - t.j0);
                     if (t.j1 > blocks || (t.ends != (t.j1 == blocks))) fail("ends", t.j1, blocks);
                     if (!t.ends && t.j1 <= t.j0) fail("nothing taken", t.j0, t.j1);
                     inside += !t.begins;
