@@ -256,11 +256,11 @@ template <> constexpr float kLift<__nv_bfloat16> = 0.0f;
 
 // ------------------------------------------------------------- the layout ---
 
-// Shared memory, D = 64 or 128: queries of two tiles (kQ of them), the ring, 1 KB for each softmax warp.
+// Shared memory, D = 64 or 128: queries of two tiles (kQ of them), the ring.
 template <int D> constexpr int kTileBytes = kRows * D * 2;    // of queries, of a block of keys or values
 template <int D> constexpr int kQ = D == 64 ? 2 : 1;
-template <int D> constexpr int kStages = D == 64 ? 7 : 4;
-template <int D> constexpr int kSmem = 1024 + kQ<D> * 2 * kTileBytes<D> + kStages<D> * kTileBytes<D> + kSoftmaxWarps * 1024;
+template <int D> constexpr int kStages = D == 64 ? 10 : 5;
+template <int D> constexpr int kSmem = 1024 + kQ<D> * 2 * kTileBytes<D> + kStages<D> * kTileBytes<D>;
 
 __device__ __forceinline__ int seen_by(const Piece& p, bool causal, int token) {
     if (!causal) return p.keys;
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __shared__ volatile int not_finite[kFlags];   // the item (by number of pieces) in whose masked blocks values were replaced
     uint8_t* const base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t queries = smem_u32(base), ring = queries + NQ * 2 * kTileBytes<D>;
-    uint8_t* const passes = base + NQ * 2 * kTileBytes<D> + ST * kTileBytes<D>;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (ST + s); };
@@ -509,24 +508,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint32_t tm = (uint32_t)same((int)tmem), queries_u = (uint32_t)same((int)queries), ring_u = (uint32_t)same((int)ring);
         int j0 = 0, j1 = 0, end0 = 0, end1 = 0, seen0 = 0, seen1 = 0;               // the piece whose P V come next
         int next_j0 = 0, next_j1 = 0, next_end0 = 0, next_end1 = 0, next_seen0 = 0, next_seen1 = 0;   // the one after it
-        // that one: the next that has blocks
+        bool ok = true;
+        // That one, and whether it has blocks.  (Not the next that has some: between them more pieces may lie than
+        // there are places for, and those are free only once this piece's products are done.)
+        enum { kEnd, kBlocks, kNothing };
         auto look_ahead = [&] {
-            do {
-                const int at = number % kPieces;
-                if (!wait_all(piece_full(at), (number / kPieces) & 1)) return false;
-                const Piece& c = pieces[at];
-                next_j0 = same(c.j0);
-                next_j1 = same(c.j1);
-                next_end0 = same(c.end0);
-                next_end1 = same(c.end1);
-                next_seen0 = same(c.seen0);
-                next_seen1 = same(c.seen1);
-                __syncwarp();
-                if (lane == 0) arrive(piece_empty(at));
-                if (next_j0 < 0) return false;
-                ++number;
-            } while (next_j1 <= next_j0);
-            return true;
+            const int at = number % kPieces;
+            ok = wait_all(piece_full(at), (number / kPieces) & 1);
+            if (!ok) return kEnd;
+            const Piece& c = pieces[at];
+            next_j0 = same(c.j0);
+            next_j1 = same(c.j1);
+            next_end0 = same(c.end0);
+            next_end1 = same(c.end1);
+            next_seen0 = same(c.seen0);
+            next_seen1 = same(c.seen1);
+            __syncwarp();
+            if (lane == 0) arrive(piece_empty(at));
+            if (next_j0 < 0) return kEnd;
+            ++number;
+            return next_j1 > next_j0 ? kBlocks : kNothing;
         };
         auto go_on = [&] {
             j0 = next_j0;
@@ -562,61 +563,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             commit(summed(t));
         };
-        bool ok = look_ahead();
-        if (ok) {
-            go_on();
-            ok = wait_all(q_full(0), 0) && wait_all(full(s), phase);
-            if (ok) {
-                tmem_fence_after();
-                if (j0 < end0) score(0, seen0, j0, 0, s);
-                if (j0 < end1) score(1, seen1, j0, 0, s);
-                advance();
-                if (j0 + 1 == j1) commit(q_empty(0));
+        auto next = look_ahead();
+        while (ok && next != kEnd) {
+            if (next == kNothing) {
+                next = look_ahead();
+                continue;
             }
-        }
-        while (ok) {
-            bool more = false;
-            for (int j = j0; j < j1 && ok; ++j) {
-                const int v_stage = s;
-                ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
-                if (!ok) break;
-                // the block whose scores come next: this piece's, or the first of the next one
-                const bool inside = j + 1 < j1;
-                more = inside || look_ahead();
-                const int then_j = inside ? j + 1 : next_j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
-                const int then_end0 = inside ? end0 : next_end0, then_end1 = inside ? end1 : next_end1;
-                const int k_stage = s + 1 == ST ? 0 : s + 1;
-                const uint32_t k_phase = s + 1 == ST ? phase ^ 1u : phase;
-                if (j < end0) {
-                    ok = wait_all(weights(0), weights_phase0);
-                    weights_phase0 ^= 1u;
+            // a piece that does not follow on another's products
+            go_on();
+            ok = wait_all(q_full(item % NQ), (item / NQ) & 1) && wait_all(full(s), phase);
+            if (!ok) break;
+            tmem_fence_after();
+            if (j0 < end0) score(0, seen0, j0, item % NQ, s);
+            if (j0 < end1) score(1, seen1, j0, item % NQ, s);
+            advance();
+            if (j0 + 1 == j1) commit(q_empty(item % NQ));
+            for (;;) {
+                for (int j = j0; j < j1 && ok; ++j) {
+                    const int v_stage = s;
+                    ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
                     if (!ok) break;
-                    tmem_fence_after();
-                    weigh(0, seen0, j, v_stage, j > j0);
-                }
-                if (more) {
-                    ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
+                    // the block whose scores come next: this piece's, or the first of the next one
+                    const bool inside = j + 1 < j1;
+                    if (!inside) next = look_ahead();
                     if (!ok) break;
-                    tmem_fence_after();
-                    if (then_j < then_end0) score(0, inside ? seen0 : next_seen0, then_j, qs, k_stage);
-                }
-                if (j < end1) {
-                    ok = wait_all(weights(1), weights_phase1);
-                    weights_phase1 ^= 1u;
-                    if (!ok) break;
-                    tmem_fence_after();
-                    weigh(1, seen1, j, v_stage, j > j0);
-                }
-                if (more && then_j < then_end1) score(1, inside ? seen1 : next_seen1, then_j, qs, k_stage);
-                advance();
-                if (more) {
+                    const bool more = inside || next == kBlocks;
+                    const int then_j = inside ? j + 1 : next_j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
+                    const int then_end0 = inside ? end0 : next_end0, then_end1 = inside ? end1 : next_end1;
+                    const int k_stage = s + 1 == ST ? 0 : s + 1;
+                    const uint32_t k_phase = s + 1 == ST ? phase ^ 1u : phase;
+                    if (j < end0) {
+                        ok = wait_all(weights(0), weights_phase0);
+                        weights_phase0 ^= 1u;
+                        if (!ok) break;
+                        tmem_fence_after();
+                        weigh(0, seen0, j, v_stage, j > j0);
+                    }
+                    if (more) {
+                        ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
+                        if (!ok) break;
+                        tmem_fence_after();
+                        if (then_j < then_end0) score(0, inside ? seen0 : next_seen0, then_j, qs, k_stage);
+                    }
+                    if (j < end1) {
+                        ok = wait_all(weights(1), weights_phase1);
+                        weights_phase1 ^= 1u;
+                        if (!ok) break;
+                        tmem_fence_after();
+                        weigh(1, seen1, j, v_stage, j > j0);
+                    }
+                    if (more && then_j < then_end1) score(1, inside ? seen1 : next_seen1, then_j, qs, k_stage);
                     advance();
-                    if (then_j + 1 == (inside ? j1 : next_j1)) commit(q_empty(qs));
+                    if (more) {
+                        advance();
+                        if (then_j + 1 == (inside ? j1 : next_j1)) commit(q_empty(qs));
+                    }
                 }
+                ++item;
+                if (!ok || next != kBlocks) break;
+                go_on();
             }
-            if (!more) break;
-            go_on();
-            ++item;
         }
         if (last != 0) bar_drain(last, last_phase);   // the last products are done before TMEM is freed
         __syncwarp();
@@ -770,60 +776,46 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 // what only this end of a piece needs is made here, not kept in registers meanwhile
                 int me = threadIdx.x - 128;
                 asm volatile("" : "+r"(me));
-                uint8_t* const pass = passes + (me >> 5) * 1024;
                 const int member = (me & 127) - token * p.group;
                 const bool whole = c.slot < 0;
                 const int part_row = max(c.slot, 0) * p.slot_rows + tile * kRows + row;
                 if (!whole && mine) p.stats[part_row] = make_float2(any ? ms : -INFINITY, any ? l : 0.0f);
                 const float inverse = !any || seen == 0 ? 0.0f : whole ? 1.0f / l : 1.0f;
-                // where this row goes, for the lanes that write it; rows of nothing go nowhere
-                const char* const to = !mine           ? nullptr
-                                       : whole ? static_cast<const char*>(p.out) + ((long long)(c.q0 + here) * p.out_stride +
-                                                                                     ((long long)c.head * p.group + member) * p.dim) * 2
-                                               : reinterpret_cast<const char*>(p.parts + (long long)part_row * D);
+                char* const to = whole ? static_cast<char*>(p.out) + ((long long)(c.q0 + here) * p.out_stride +
+                                                                     ((long long)c.head * p.group + member) * p.dim) * 2
+                                       : reinterpret_cast<char*>(p.parts + (long long)part_row * D);
                 const int until = p.dim;
-                const int at_lane = me & 31;
-                uint4* const line = reinterpret_cast<uint4*>(pass) + at_lane * 2;
-                const uint4* const from = reinterpret_cast<const uint4*>(pass) + (at_lane >> 1) * 2 + ((at_lane & 1) ^ (at_lane >> 3 & 1));
                 if (whole || any) {
 #pragma unroll 1
-                    for (int g = 0; g < until; g += 8) {
-                        uint32_t o[8];
-                        tmem_load(tm + 2 * kKeys + tile * D + g, o);
+                    for (int g = 0; g < until; g += 32) {
+                        uint32_t o[32];
+                        tmem_load32(tm + 2 * kKeys + tile * D + g, o);
                         tmem_wait(o);
                         // (a row that sees nothing gets zeros, whatever its sums are)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = inverse == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inverse);
-                        // through the warp's 1 KB, so that rows are written in runs of 32 bytes; 16-byte piece q of
-                        // row r lies at q ^ (r >> 2 & 1): no bank conflicts
-                        const int turned = lane >> 2 & 1;
-                        if (whole) {
-                            line[(g >> 3 & 1) ^ turned] = make_uint4(pack2<E>(__uint_as_float(o[0]), __uint_as_float(o[1])),
-                                                                     pack2<E>(__uint_as_float(o[2]), __uint_as_float(o[3])),
-                                                                     pack2<E>(__uint_as_float(o[4]), __uint_as_float(o[5])),
-                                                                     pack2<E>(__uint_as_float(o[6]), __uint_as_float(o[7])));
-                            if ((g & 8) == 0 && g + 8 < until) continue;   // the line's other half follows
-                        } else {
-                            line[turned] = make_uint4(o[0], o[1], o[2], o[3]);
-                            line[turned ^ 1] = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                        __syncwarp();
-                        const int at = whole ? ((g & ~8) + (lane & 1) * 8) * 2 : (g + (lane & 1) * 4) * 4;
-                        const bool in = !whole || (g & ~8) + (lane & 1) * 8 < until;
+                        for (int i = 0; i < 32; ++i) o[i] = inverse == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inverse);
+                        auto two_of = [&](int i) { return pack2<E>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])); };
+                        if (mine) {
+                            if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 v = from[i * 32];
-                            const char* const row_to = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, (unsigned long long)to, i * 16 + (lane >> 1)));
-                            if (in && row_to != nullptr) *reinterpret_cast<uint4*>(const_cast<char*>(row_to) + at) = v;
+                                for (int i = 0; i < 4; ++i)
+                                    if (g + 8 * i < until)
+                                        *reinterpret_cast<uint4*>(to + (g + 8 * i) * 2) =
+                                            make_uint4(two_of(8 * i), two_of(8 * i + 2), two_of(8 * i + 4), two_of(8 * i + 6));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (g + 4 * i < until)
+                                        *reinterpret_cast<uint4*>(to + (g + 4 * i) * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            }
                         }
-                        __syncwarp();
                     }
                     tmem_fence_before();   // O is read: the next item's products may overwrite it
                 }
                 if (any && not_finite[number % kFlags] == number && mine) {
                     // values of masked blocks that are not finite, for the rows that see them: added to what was written
                     const int first = max(begin, least / kKeys) * kKeys, end = min(seen, e * kKeys);
-                    char* const out = const_cast<char*>(to);
+                    char* const out = to;
 #pragma unroll 1
                     for (int k = first; k < end; ++k) {
                         const E* const v = static_cast<const E*>(p.values) + (long long)(c.k0 + k) * p.v_stride + (long long)c.head * p.dim;

@@ -32,6 +32,62 @@ struct LayerParams {
     float eps;
 };
 
+// Sum over the T threads of a row, and likewise the largest bits and two sums, in a fixed order.  Rows of several
+// warps pass through `between`, one of its own for each reduction that may follow before all threads have read
+// it: one barrier each.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* between) {
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = between[0];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) v += between[i];
+    }
+    return v;
+}
+template <int T>
+__device__ __forceinline__ unsigned row_top(unsigned v, float* between) {
+    if constexpr (T < 32) {
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    } else {
+        v = __reduce_max_sync(0xffffffffu, v);
+    }
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = __uint_as_float(v);
+        __syncthreads();
+        v = __float_as_uint(between[0]);
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) v = max(v, __float_as_uint(between[i]));
+    }
+    return v;
+}
+template <int T>
+__device__ __forceinline__ float2 row_sums(float a, float b, float2* between) {
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        float2 v = between[0];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) {
+            const float2 w = between[i];
+            v.x += w.x;
+            v.y += w.y;
+        }
+        return v;
+    }
+    return make_float2(a, b);
+}
+template <int T> constexpr int kRowWarps = T > 32 ? T / 32 : 1;
+
 // CTAs of one-warp rows that an SM is to hold: enough rows under way, without spills.
 template <int V, int T, bool Q8>
 constexpr int kLayerResident = T > 32 || V == 1 ? 1 : Q8 ? 3 : V == 8 ? 4 : 2;
@@ -65,7 +121,8 @@ __global__ void __launch_bounds__(kThreads<T>, kLayerResident<V, T, Q8>) layer_k
     }
     if (T == 32 && !some) return;
     float h[NV][V];
-    float sum = 0.0f, none = 0.0f;
+    __shared__ float between[3][kRowWarps<T>];   // of the sum, the squares, the maximum
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -83,8 +140,7 @@ __global__ void __launch_bounds__(kThreads<T>, kLayerResident<V, T, Q8>) layer_k
             store_pack<E, V>(ho, i * T * V + c0, n, o);
         }
     }
-    reduce_row<T, false>(sum, none);
-    const float mean = sum / (float)n;
+    const float mean = row_sum<T>(sum, between[0]) / (float)n;
     float squares = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -103,9 +159,7 @@ __global__ void __launch_bounds__(kThreads<T>, kLayerResident<V, T, Q8>) layer_k
             }
         }
     }
-    none = 0.0f;
-    reduce_row<T, false>(squares, none);
-    const float s = rsqrtf(squares / (float)n + p.eps);
+    const float s = rsqrtf(row_sum<T>(squares, between[1]) / (float)n + p.eps);
     float w[V], b[V];
     unsigned top = 0;   // |.| as bits: orders like the values, infinities and NaN on top
 #pragma unroll
@@ -128,9 +182,7 @@ __global__ void __launch_bounds__(kThreads<T>, kLayerResident<V, T, Q8>) layer_k
         }
     }
     if constexpr (Q8) {
-        float a = __uint_as_float(top);
-        none = 0.0f;
-        reduce_row<T, true>(none, a);
+        const float a = __uint_as_float(row_top<T>(top, between[2]));
         const bool finite = __float_as_uint(a) < 0x7f800000u;
         const float k = finite && a >= kTiny ? 127.0f / a : 0.0f;
         if (t == 0 && some) p.scale[row] = !finite ? __uint_as_float(0x7fffffffu) : a >= kTiny ? a / 127.0f : 0.0f;
@@ -299,6 +351,8 @@ __global__ void __launch_bounds__(kThreads<T>) layer_grad_kernel(const LayerGrad
         }
         return load_pack<E, V>(static_cast<const E*>(base) + row * stride, c, n, false);
     };
+    __shared__ float2 between[2][2][kRowWarps<T>];   // of the two reductions, for even and odd rows
+    int turn = 0;
     Two dw[N / 2], db[N / 2], w[N / 2];
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
@@ -322,19 +376,19 @@ __global__ void __launch_bounds__(kThreads<T>) layer_grad_kernel(const LayerGrad
         auto pair = [&](const Pack<E, V> (&v)[NV], int e) {
             return two(to_f(v[e / V].e[e % V]), to_f(v[(e + 1) / V].e[(e + 1) % V]));
         };
-        Two u[N / 2];
+        Two u[N / 2], y[N / 2];
         Two h2 = two(0.0f, 0.0f), g2 = two(0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             u[e / 2] = pair(ph, e);
+            y[e / 2] = pair(py, e);
             h2 = add_two(u[e / 2], h2);
-            g2 = fma_two(pair(py, e), w[e / 2], g2);
+            g2 = fma_two(y[e / 2], w[e / 2], g2);
         }
         fetch(slot);   // the packs are in registers
         if (++slot >= AHEAD) slot = 0;
-        float hs = apart(h2).x + apart(h2).y, gs = apart(g2).x + apart(g2).y;
-        reduce_row<T, false>(hs, gs);
-        const float mean = hs / (float)n;
+        const float2 first = row_sums<T>(apart(h2).x + apart(h2).y, apart(g2).x + apart(g2).y, between[turn][0]);
+        const float mean = first.x / (float)n, gs = first.y;
         const Two less = two(-mean, -mean);
         Two uu2 = two(0.0f, 0.0f), gu2 = two(0.0f, 0.0f);
 #pragma unroll
@@ -345,10 +399,11 @@ __global__ void __launch_bounds__(kThreads<T>) layer_grad_kernel(const LayerGrad
                 u[e / 2] = two(mask >> e & 1 ? v.x : 0.0f, mask >> (e + 1) & 1 ? v.y : 0.0f);
             }
             uu2 = fma_two(u[e / 2], u[e / 2], uu2);
-            gu2 = fma_two(mul_two(pair(py, e), w[e / 2]), u[e / 2], gu2);
+            gu2 = fma_two(mul_two(y[e / 2], w[e / 2]), u[e / 2], gu2);
         }
-        float uu = apart(uu2).x + apart(uu2).y, gu = apart(gu2).x + apart(gu2).y;
-        reduce_row<T, false>(uu, gu);
+        const float2 next = row_sums<T>(apart(uu2).x + apart(uu2).y, apart(gu2).x + apart(gu2).y, between[turn][1]);
+        const float uu = next.x, gu = next.y;
+        turn ^= 1;
         // dx = s g - (s^3 gu / n) u + (dres - s gs / n)
         const float s = rsqrtf(uu / (float)n + p.eps), along = -(gu / (float)n * s * s * s), level = -(gs / (float)n * s);
         const Two s2 = two(s, s), along2 = two(along, along), level2 = two(level, level);
@@ -359,9 +414,8 @@ __global__ void __launch_bounds__(kThreads<T>) layer_grad_kernel(const LayerGrad
             for (int j = 0; j < V; j += 2) {
                 // (V = 1: pairs are of two packs; the second pack's half is made with it)
                 const int e = V > 1 ? i * V + j : i / 2 * 2;
-                const Two y = pair(py, e);
                 const Two r = p.dresidual != nullptr ? add_two(pair(pr, e), level2) : level2;
-                const float2 d = apart(fma_two(s2, mul_two(y, w[e / 2]), fma_two(along2, u[e / 2], r)));
+                const float2 d = apart(fma_two(s2, mul_two(y[e / 2], w[e / 2]), fma_two(along2, u[e / 2], r)));
                 if constexpr (V > 1) {
                     o.e[j] = from_f<E>(d.x);
                     o.e[j + 1] = from_f<E>(d.y);
@@ -369,8 +423,8 @@ __global__ void __launch_bounds__(kThreads<T>) layer_grad_kernel(const LayerGrad
                     o.e[0] = from_f<E>(i % 2 ? d.y : d.x);
                 }
                 if (V > 1 || i % 2 == 0) {
-                    dw[e / 2] = fma_two(y, mul_two(u[e / 2], s2), dw[e / 2]);
-                    db[e / 2] = add_two(y, db[e / 2]);
+                    dw[e / 2] = fma_two(y[e / 2], mul_two(u[e / 2], s2), dw[e / 2]);
+                    db[e / 2] = add_two(y[e / 2], db[e / 2]);
                 }
             }
             store_pack<E, V>(dx, i * T * V + c0, n, o);

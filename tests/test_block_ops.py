@@ -673,6 +673,21 @@ def test_attention_many_sequences():
 
 
 @gpu
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_of_empty_sequences_between_long_ones(dim):
+    """Many items in a row that have no keys, or few, between items that have: more than there are places for
+    what a part of the kernel tells the others."""
+    p = Problem(dim, [1] * 24, [2000] * 12 + [0] + [2000] * 11, 32, 16, dim, torch.bfloat16)
+    p.check(p.run(True), True)
+    p = Problem(dim, [300] + [40] * 20 + [2] * 9, [700] + [0] * 20 + [500] * 9, 12, 12, dim, torch.float16)
+    p.check(p.run(False), False)
+    p = Problem(dim, [500, 90, 700, 3, 800], [100, 0, 900, 1, 300], 24, 24, dim, torch.float16)
+    p.check(p.run(True), True)
+    p.buf.check_around()
+    assert trfn.tr_device_status() == 0
+
+
+@gpu
 @pytest.mark.parametrize("dtype", TYPES, ids=name_of)
 @pytest.mark.parametrize("sharp", [0.0, 8.0, 100.0])
 def test_attention_of_even_and_sharp_scores(sharp, dtype):
