@@ -1,7 +1,10 @@
 """From a uint8 image batch to a network's hidden rows, on the GPU: the fused
 normalisation, its patches in 8 bits, the patch embedding as an 8-bit integer
-product, and one pre-norm block (RMS norm with the residual's addition, 8-bit
-output; two products), then a training step's gradients of a norm.
+product, one pre-norm block (RMS norm with the residual's addition, 8-bit
+output; two products), an attention block among each image's patches (layer norm
+with 8-bit output, the product for queries, keys and values, rotary positions,
+attention, a product, layer norm with the residual's addition), then a training
+step's gradients of the norms and positions.
 
     python examples/image_tokens.py [images] [width]
 """
@@ -68,6 +71,50 @@ def forward(net, rows, positions):
     return y, h2
 
 
+HEAD = 64
+
+
+def build_attention(width, seed=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def matrix(n, k):
+        return torch.randn((n, k), generator=g, device="cuda") / k ** 0.5
+
+    ones, zeros = torch.ones(width, device="cuda"), torch.zeros(width, device="cuda")
+    return {"qkv": Linear8(matrix(3 * width, width)), "out": Linear8(matrix(width, width)), "weight1": ones, "bias1": zeros,
+            "weight2": ones, "bias2": zeros, "freqs": trfn.tr_rotary_frequencies(HEAD)[0], "workspace": None}
+
+
+def attend(net, x, images):
+    """x and what the patches of each image tell one another, normalised; and the sum before the norm."""
+    rows, width = x.shape
+    heads, patches_an_image = width // HEAD, rows // images
+    q8, scale = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    trfn.tr_layer_norm(x, q8, weight=net["weight1"], bias=net["bias1"], scale=scale)
+    qkv = net["qkv"](q8, scale)
+    # queries and keys are neighbours in the product's rows: their heads turn together, in place
+    at = torch.arange(rows, dtype=torch.int32, device="cuda") % patches_an_image
+    trfn.tr_rotary(qkv[:, :2 * width], qkv[:, :2 * width], 2 * heads, net["freqs"], positions=at)
+    starts = torch.arange(images + 1, dtype=torch.int32, device="cuda") * patches_an_image
+    need = trfn.tr_attention_workspace_bytes(rows, images, heads, heads, HEAD)
+    if net["workspace"] is None or net["workspace"].numel() < need:
+        net["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda")
+    mixed = torch.empty_like(x)
+    trfn.tr_attention(qkv[:, :width], qkv[:, width:2 * width], qkv[:, 2 * width:], mixed, heads, heads, starts,
+                      workspace=net["workspace"])
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    trfn.tr_layer_norm(net["out"](*quantised(mixed)), y, weight=net["weight2"], bias=net["bias2"], residual=x, residual_out=h)
+    return y, h
+
+
+def layer_norm_gradients(dy, h, weight):
+    rows, cols = h.shape
+    dx, dweight, dbias = torch.empty_like(h), torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    workspace = torch.empty(trfn.tr_layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    trfn.tr_layer_norm_backward(dy, h, dx, weight=weight, dweight=dweight, dbias=dbias, workspace=workspace)
+    return dx, dweight, dbias
+
+
 def norm_gradients(dy, h, weight):
     rows, cols = h.shape
     dx, dweight = torch.empty_like(h), torch.empty(cols, device="cuda")
@@ -97,6 +144,10 @@ def main(images=8, width=512):
     positions = 0.02 * torch.randn((rows.size(0), width), device="cuda", dtype=torch.bfloat16)
     y, h = forward(net, rows, positions)
     dx, dweight = norm_gradients(torch.ones_like(y), h, net["norm2"])
+    if width % HEAD == 0:
+        net2 = build_attention(width)
+        y, h = attend(net2, y, images)
+        dx, dweight, _ = layer_norm_gradients(torch.ones_like(y), h, net2["weight2"])
     torch.cuda.synchronize()
     print("%d images -> %d tokens of %d; hidden rms %.4f, |dx| %.4g, |dweight| %.4g" % (
         images, rows.size(0), width, y.float().square().mean().sqrt().item(), dx.float().norm().item(), dweight.norm().item()))

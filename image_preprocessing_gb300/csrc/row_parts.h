@@ -161,6 +161,62 @@ __device__ __forceinline__ void reduce_row(float& a, float& b) {
     }
 }
 
+// Sum over the T threads of a row, and likewise the largest bits and two sums, in a fixed order.  Rows of several
+// warps pass through `between`, one of its own for each reduction that may follow before all threads have read
+// it: one barrier each.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* between) {
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = between[0];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) v += between[i];
+    }
+    return v;
+}
+template <int T>
+__device__ __forceinline__ unsigned row_top(unsigned v, float* between) {
+    if constexpr (T < 32) {
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    } else {
+        v = __reduce_max_sync(0xffffffffu, v);
+    }
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = __uint_as_float(v);
+        __syncthreads();
+        v = __float_as_uint(between[0]);
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) v = max(v, __float_as_uint(between[i]));
+    }
+    return v;
+}
+template <int T>
+__device__ __forceinline__ float2 row_sums(float a, float b, float2* between) {
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) between[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        float2 v = between[0];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) {
+            const float2 w = between[i];
+            v.x += w.x;
+            v.y += w.y;
+        }
+        return v;
+    }
+    return make_float2(a, b);
+}
+template <int T> constexpr int kRowWarps = T > 32 ? T / 32 : 1;
+
 // v rounded to the nearest integer, ties to even, for |v| <= 2^22: the low bits of v + 1.5 * 2^23 (the
 // conversion instruction takes several times as long).
 __device__ __forceinline__ uint32_t round_bits(float v) { return __float_as_uint(__fadd_rn(v, 12582912.0f)); }

@@ -17,15 +17,16 @@ the type where it is rounded (2^-25 at least in binary16, of weights whose large
 is 1 or more); sums over n keys by n/16 steps of 2^-22.  All of it relative to
 sum p |v| / sum p.  Every bound adds the rounding to the output's type."""
 import ctypes
-import importlib.util
 import math
 import os
+import subprocess
+import time
 
 import pytest
 import torch
 
 import image_preprocessing_gb300 as trfn
-from image_preprocessing_gb300 import TrError, _native
+from image_preprocessing_gb300 import TrError, _native, build
 
 OK, INVALID, NOT_SUPPORTED = 0, 1, 2
 UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
@@ -927,3 +928,116 @@ def test_binding_refusals():
         trfn.tr_layer_norm(q, out, bias=torch.ones(64, device="cuda"))
     with pytest.raises(TrError):
         trfn.tr_layer_norm_backward(q, q, out, dbias=torch.ones(128, device="cuda"))
+
+
+# ------------------------------------------------- waits, streams and kernels before ---
+
+@pytest.fixture(scope="module")
+def early_release(tmp_path_factory):
+    """early_release(out, ns): fills an int8 tensor ns after it has let the next kernel start."""
+    path = str(tmp_path_factory.mktemp("early") / "early_release.so")
+    source = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c_abi", "early_release.cu")
+    subprocess.run([build._nvcc(), "-shared", *build.ARCH, "-O2", "-Xcompiler", "-fPIC", "-o", path, source], check=True)
+    fn = ctypes.CDLL(path).early_release
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_ulonglong, ctypes.c_void_p]
+    return lambda out, ns: fn(out.data_ptr(), out.numel(), ns, torch.cuda.current_stream().cuda_stream)
+
+
+@gpu
+@pytest.mark.parametrize("what", ["layer_norm", "layer_norm_backward", "rotary", "attention", "plain_attention"])
+def test_a_kernel_that_releases_early_is_waited_for(early_release, what):
+    """The kernel before lets the operator start and writes its input last of all, after longer than the limit of
+    the operator's own waits."""
+    rows, cols = 300, 256
+    raw = torch.zeros(rows * cols * 2, dtype=torch.int8, device="cuda")
+    x, out = raw.view(torch.bfloat16).view(rows, cols), torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    starts = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    ws = torch.empty(trfn.tr_attention_workspace_bytes(rows, 2, 4, 4, 64), dtype=torch.uint8, device="cuda")
+    freqs, _ = trfn.tr_rotary_frequencies(64)
+
+    def run():
+        if what == "layer_norm":
+            trfn.tr_layer_norm(x, out)
+        elif what == "layer_norm_backward":
+            trfn.tr_layer_norm_backward(x, x, out)
+        elif what == "rotary":
+            trfn.tr_rotary(x, out, 4, freqs)
+        elif what == "attention":
+            trfn.tr_attention(x, x, x, out, 4, 4, starts, workspace=ws, scale=1e-3)
+        else:
+            trfn.tr_attention(x, x, x, out, 4, 4, starts, workspace=ws, scale=-1e-3)
+
+    torch.cuda.synchronize()
+    assert early_release(raw, 1_500_000_000) == 0
+    run()
+    torch.cuda.synchronize()
+    got = out.clone()
+    filled = (torch.arange(raw.numel(), device="cuda") * 7 % 251 - 125).to(torch.int8)
+    assert torch.equal(raw, filled)
+    out.zero_()
+    run()
+    assert torch.equal(got.view(torch.int16), out.view(torch.int16)) and trfn.tr_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_whose_wait_runs_out(dim):
+    """The first stage of the first CTA waits for an arrival that never comes (tr_tune_tiled's test hook): the
+    launch ends by itself and reports it, and what it has written is right."""
+    p = Problem(dim, [1500, 40, 900], [1500, 40, 900], 8, 4, dim, torch.bfloat16)
+    want = p.run(False).clone()
+    out = torch.full_like(want, float("nan"))
+    assert trfn.tr_device_status(clear=True) == 0
+    try:
+        trfn.tr_tune_tiled(0, 0, 0, 64)
+        t0 = time.perf_counter()
+        p.run(False, out=out)
+        torch.cuda.synchronize()
+        elapsed = time.perf_counter() - t0
+    finally:
+        trfn.tr_tune_tiled(0, 0, 0, 0)
+    assert 0.5 < elapsed < 30
+    assert trfn.tr_device_status(clear=True) == 1
+    written = ~out.isnan()
+    assert not bool(written[0, 0]) and bool(written.any())
+    assert torch.equal(out[written], want[written])
+    assert torch.equal(p.run(False), want) and trfn.tr_device_status() == 0
+
+
+@gpu
+def test_two_streams_with_workspaces_of_their_own():
+    problems = [Problem(s, [900, 3, 200], [900, 3, 200], 8, 2, 128, torch.bfloat16) for s in (1, 2)]
+    want = [p.run(True).clone() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    args = []
+    for p in problems:
+        n = trfn.tr_attention_workspace_bytes(p.q.size(0), 3, 8, 2, 128)
+        args.append((p, p.arrays(), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.zeros_like(p.out)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (p, arrays, ws, out) in zip(streams, args):
+            trfn.tr_attention(p.q, p.k, p.v, out, 8, 2, causal=True, workspace=ws, stream=s, **arrays)
+    torch.cuda.synchronize()
+    for (p, _, _, out), w in zip(args, want):
+        assert torch.equal(out, w)
+    assert trfn.tr_device_status() == 0
+
+
+@gpu
+def test_attention_again_and_again_is_the_same():
+    """Many launches one after the other, over sequences of every kind, with one workspace."""
+    g = torch.Generator().manual_seed(11)
+    for _ in range(12):
+        n = int(torch.randint(1, 40, (1,), generator=g))
+        kv, group, dim = [(1, 8, 128), (8, 1, 64), (4, 3, 96), (2, 5, 64)][int(torch.randint(0, 4, (1,), generator=g))]
+        top = int(torch.randint(1, 1200, (1,), generator=g))
+        lk = (torch.randint(0, top, (n,), generator=g) * (torch.rand(n, generator=g) < 0.8)).tolist()
+        lq = lk if torch.rand(1, generator=g) < 0.5 else [1 + i % 3 for i in range(n)]
+        p = Problem(n, lq, lk, kv * group, kv, dim, torch.float16)
+        if sum(lq) == 0:
+            continue
+        first = p.run(True).clone()
+        p.check(first, True)
+        for _ in range(25):
+            assert torch.equal(p.run(True), first)
+    assert trfn.tr_device_status() == 0
