@@ -284,23 +284,26 @@ struct PlanParams {
 constexpr int kPlanThreads = 256;
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-    __shared__ long long upto[kPlanThreads];   // units of the chunk's sequences, up to each
+    __shared__ long long upto[kPlanThreads], warps[kPlanThreads / 32];   // units of the chunk's sequences, up to each
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int n = p.seq.count, t = threadIdx.x;
     auto sequence = [&](int s) {
         return attention::Sequence{range_of(p.seq.q_starts, p.seq.q_lengths, s, p.seq.q_rows).length,
                                    range_of(p.seq.k_starts, p.seq.k_lengths, s, p.seq.k_rows).length, p.tokens, p.causal};
     };
-    auto scan = [&](long long mine) {   // leaves the sums in upto
-        __syncthreads();
-        upto[t] = mine;
-        __syncthreads();
-        for (int o = 1; o < kPlanThreads; o <<= 1) {
-            const long long left = t >= o ? upto[t - o] : 0;
-            __syncthreads();
-            upto[t] += left;
-            __syncthreads();
+    auto scan = [&](long long v) {   // leaves the sums in upto
+        const int lane = t & 31;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long left = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += left;
         }
+        __syncthreads();   // the last chunk's sums have been read
+        if (lane == 31) warps[t >> 5] = v;
+        __syncthreads();
+        for (int w = 0; w < (t >> 5); ++w) v += warps[w];
+        upto[t] = v;
+        __syncthreads();
     };
     long long mine = 0;
     for (int s = t; s < n; s += kPlanThreads) mine += sequence(s).head_units() * p.kv_heads;
@@ -859,11 +862,12 @@ struct JoinParams {
     bool causal;
 };
 
-constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+constexpr int kJoinWarps = 8, kJoinBlocks = 16;
 
 // The pieces of the item that CTA blockIdx.x of the attention kernel began and did not end; gridDim.y CTAs
 // share its rows.  A warp takes a row, four values a lane; where an item has many pieces (a few rows, then),
-// the CTA's warps share a row's.
+// the CTA's warps share a row's.  Latency counts: slots, maxima and sums are read by a lane each, and the
+// pieces' values four at a time.
 template <typename E, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams p) {
     __shared__ float sums[kJoinWarps][D + 1];
@@ -871,44 +875,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams 
     const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Slot head = p.slots[2 * c0 + 1];
     if (head.state != kFirst) return;
-    // pieces: this one's slot 2 c0 + 1, then slots 2 c of the CTAs after it; one that has none of it is passed over
-    int last = c0;
-    bool whole = true;
-    for (int c = c0 + 1; c < kCtas; ++c) {
-        const Slot s = p.slots[2 * c];
-        if (s.state & kFailed) whole = false;
-        last = c;
-        if ((s.state & kNext) && s.ends) break;
+    // pieces: this one's slot 2 c0 + 1, then slots 2 c of the CTAs after it, up to the one that ends the item; a
+    // CTA that has none of it is passed over.  Nothing is stored where a wait that ran out left one unfinished.
+    int n = 0;
+    for (int c = c0 + 1; c < kCtas && n == 0; c += 32) {
+        int state = 0, ends = 0;
+        if (c + lane < kCtas) {
+            state = p.slots[2 * (c + lane)].state;
+            ends = p.slots[2 * (c + lane)].ends;
+        }
+        const unsigned end = __ballot_sync(0xffffffffu, (state & kNext) != 0 && ends != 0);
+        const unsigned upto = end != 0 ? (2u << (__ffs((int)end) - 1)) - 1 : 0xffffffffu;
+        if (__ballot_sync(0xffffffffu, (state & kFailed) != 0) & upto) return;
+        if (end != 0) n = c - c0 + __ffs((int)end);
     }
-    if (!whole) return;   // not stored, like the rest of what a wait that ran out left unfinished
-    const int n = last - c0 + 1;
+    if (n == 0) return;   // (not reached: some CTA ends the item)
     auto slot_of = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
     const bool shared = n > kJoinWarps;
     const int first = shared ? blockIdx.y : blockIdx.y * kJoinWarps + warp, step = shared ? gridDim.y : gridDim.y * kJoinWarps;
+    // whether piece `lane` (the first 32) has anything of the item
+    const bool there = lane == 0 || (lane < n && p.slots[slot_of(min(lane, n - 1))].state == kNext);
     for (int tile = 0; tile < 2; ++tile) {
         const int tokens = min(p.tokens, head.tokens - tile * p.tokens);
         for (int row = first; row < tokens * p.group; row += step) {
             const int token = row / p.group, member = row - token * p.group, at = tile * kRows + row;
             auto stat = [&](int i) {
-                return i == 0 || p.slots[slot_of(i)].state == kNext ? p.stats[(long long)slot_of(i) * p.slot_rows + at] : make_float2(-INFINITY, 0.0f);
+                const bool has = i < n && (i < 32 ? there : p.slots[slot_of(i)].state == kNext);
+                return has ? p.stats[(long long)slot_of(i) * p.slot_rows + at] : make_float2(-INFINITY, 0.0f);
             };
-            float top = -INFINITY;
-            for (int i = lane; i < n; i += 32) top = fmaxf(top, stat(i).x);
+            // of the pieces lane, lane + 32, ...: the first's statistics stay
+            const float2 mine = stat(lane);
+            float top = mine.x;
+            for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, stat(i).x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             float l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int i = shared ? warp : 0; i < n; i += shared ? kJoinWarps : 1) {
-                const float2 s = stat(i);
-                // a piece whose scores are not numbers has a sum that is none; one that saw nothing has no sum
-                if (s.y == 0.0f && s.x == -INFINITY) continue;
-                const float w = s.x == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : power2(s.x - top);
-                l = fmaf(s.y, w, l);
-                if (lane * 4 < D) {
-                    const float4 v = *reinterpret_cast<const float4*>(p.parts + ((long long)slot_of(i) * p.slot_rows + at) * D + lane * 4);
-                    acc[0] = fmaf(v.x, w, acc[0]);
-                    acc[1] = fmaf(v.y, w, acc[1]);
-                    acc[2] = fmaf(v.z, w, acc[2]);
-                    acc[3] = fmaf(v.w, w, acc[3]);
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const float2 s = i0 == 0 ? mine : stat(i0 + lane);
+                // a piece whose scores are not numbers has a sum that is none; one that saw nothing has no sum, and
+                // no values that could be read
+                const bool none = s.y == 0.0f && s.x == -INFINITY;
+                const float w = none ? 0.0f : s.x == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : power2(s.x - top);
+                const unsigned has = __ballot_sync(0xffffffffu, !none);
+                const float wl = none ? 0.0f : s.y * w;
+#pragma unroll 4
+                for (int i = shared ? warp : 0; i < min(32, n - i0); i += shared ? kJoinWarps : 1) {
+                    const float wi = __shfl_sync(0xffffffffu, w, i);
+                    l += __shfl_sync(0xffffffffu, wl, i);
+                    if ((has >> i & 1) && lane * 4 < D) {
+                        const float4 v = *reinterpret_cast<const float4*>(p.parts + ((long long)slot_of(i0 + i) * p.slot_rows + at) * D + lane * 4);
+                        acc[0] = fmaf(v.x, wi, acc[0]);
+                        acc[1] = fmaf(v.y, wi, acc[1]);
+                        acc[2] = fmaf(v.z, wi, acc[2]);
+                        acc[3] = fmaf(v.w, wi, acc[3]);
+                    }
                 }
             }
             if (shared) {   // the warps' sums in order
