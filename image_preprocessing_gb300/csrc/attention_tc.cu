@@ -567,65 +567,55 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             commit(summed(t));
         };
         auto next = look_ahead();
-        while (ok && next != kEnd) {
-            if (next == kNothing) {
-                next = look_ahead();
-                continue;
-            }
-            // a piece that does not follow on another's products
+        bool follows = false;   // the piece's first scores are made beside the last one's products
+        while (ok) {
+            while (ok && next == kNothing) next = look_ahead();
+            if (!ok || next == kEnd) break;
             go_on();
-            ok = wait_all(q_full(item % NQ), (item / NQ) & 1) && wait_all(full(s), phase);
-            if (!ok) break;
-            tmem_fence_after();
-            if (j0 < end0) score(0, seen0, j0, item % NQ, s);
-            if (j0 < end1) score(1, seen1, j0, item % NQ, s);
-            advance();
-            if (j0 + 1 == j1) commit(q_empty(item % NQ));
-            for (;;) {
-                for (int j = j0; j < j1 && ok; ++j) {
-                    const int v_stage = s;
-                    ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
+            for (int j = follows ? j0 : j0 - 1; j < j1; ++j) {
+                const bool begun = j >= j0;   // else the first scores alone
+                const int v_stage = s;
+                if (begun) ok = wait_all(full(s), phase) && wait_all(clean(s), phase);
+                if (!ok) break;
+                // the block whose scores come next: this piece's, or the first of the next one
+                const bool inside = j + 1 < j1;
+                if (!inside) next = look_ahead();
+                if (!ok) break;
+                const bool more = inside || next == kBlocks;
+                const int then_j = inside ? j + 1 : next_j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
+                const int then_end0 = inside ? end0 : next_end0, then_end1 = inside ? end1 : next_end1;
+                const bool turns = begun && s + 1 == ST;
+                const int k_stage = begun ? (turns ? 0 : s + 1) : s;
+                const uint32_t k_phase = turns ? phase ^ 1u : phase;
+                if (begun && j < end0) {
+                    ok = wait_all(weights(0), weights_phase0);
+                    weights_phase0 ^= 1u;
                     if (!ok) break;
-                    // the block whose scores come next: this piece's, or the first of the next one
-                    const bool inside = j + 1 < j1;
-                    if (!inside) next = look_ahead();
-                    if (!ok) break;
-                    const bool more = inside || next == kBlocks;
-                    const int then_j = inside ? j + 1 : next_j0, then_item = inside ? item : item + 1, qs = then_item % NQ;
-                    const int then_end0 = inside ? end0 : next_end0, then_end1 = inside ? end1 : next_end1;
-                    const int k_stage = s + 1 == ST ? 0 : s + 1;
-                    const uint32_t k_phase = s + 1 == ST ? phase ^ 1u : phase;
-                    if (j < end0) {
-                        ok = wait_all(weights(0), weights_phase0);
-                        weights_phase0 ^= 1u;
-                        if (!ok) break;
-                        tmem_fence_after();
-                        weigh(0, seen0, j, v_stage, j > j0);
-                    }
-                    if (more) {
-                        ok = (inside || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
-                        if (!ok) break;
-                        tmem_fence_after();
-                        if (then_j < then_end0) score(0, inside ? seen0 : next_seen0, then_j, qs, k_stage);
-                    }
-                    if (j < end1) {
-                        ok = wait_all(weights(1), weights_phase1);
-                        weights_phase1 ^= 1u;
-                        if (!ok) break;
-                        tmem_fence_after();
-                        weigh(1, seen1, j, v_stage, j > j0);
-                    }
-                    if (more && then_j < then_end1) score(1, inside ? seen1 : next_seen1, then_j, qs, k_stage);
-                    advance();
-                    if (more) {
-                        advance();
-                        if (then_j + 1 == (inside ? j1 : next_j1)) commit(q_empty(qs));
-                    }
+                    tmem_fence_after();
+                    weigh(0, seen0, j, v_stage, j > j0);
                 }
-                ++item;
-                if (!ok || next != kBlocks) break;
-                go_on();
+                if (more) {
+                    ok = ((inside && begun) || wait_all(q_full(qs), (then_item / NQ) & 1)) && wait_all(full(k_stage), k_phase);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (then_j < then_end0) score(0, inside ? seen0 : next_seen0, then_j, qs, k_stage);
+                }
+                if (begun && j < end1) {
+                    ok = wait_all(weights(1), weights_phase1);
+                    weights_phase1 ^= 1u;
+                    if (!ok) break;
+                    tmem_fence_after();
+                    weigh(1, seen1, j, v_stage, j > j0);
+                }
+                if (more && then_j < then_end1) score(1, inside ? seen1 : next_seen1, then_j, qs, k_stage);
+                if (begun) advance();
+                if (more) {
+                    advance();
+                    if (then_j + 1 == (inside ? j1 : next_j1)) commit(q_empty(qs));
+                }
             }
+            ++item;
+            follows = next == kBlocks;
         }
         if (last != 0) bar_drain(last, last_phase);   // the last products are done before TMEM is freed
         __syncwarp();
