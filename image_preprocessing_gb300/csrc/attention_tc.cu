@@ -27,6 +27,24 @@
 //
 // A share that begins or ends inside an item leaves its sums, maxima and outputs
 // in the workspace, and a second kernel joins them in the order of the keys.
+//
+// What bounds it: the way of one block through a tile (scores 800 cycles until the
+// last is visible, weights some 1500, the products with v and the handing over)
+// is longer than the 2048 cycles that the tensor cores need for both tiles' block
+// at 128 values a head, and twice their time at 64.  Measured: 8192 causal queries,
+// 32 heads of 128 over 8 key heads, bfloat16, 504 us, 1091 TFLOP/s (0.57 of the
+// measured peak; the tensor pipe active 53 % of the cycles); 16 packed prompts of up to
+// 4096 304 us (0.41); 256 x 196, 12 heads of 64, binary16, 146 us (0.31 of the copy
+// rate); one token for each of 32 sequences over 42,000 keys in all 58 us (0.44 of
+// the copy rate; even lengths of 4096 110 us, 0.72).
+//
+// Shared memory leaves L1 a few KB, so whatever a thread keeps in local memory
+// comes from L2 each time: a kernel that spilled a few hundred bytes took five
+// times as long.  No role has a stack frame.  Tried and slower: two threads a row
+// (149 us for 138 at 4096 x 4096, 16 heads of 128), P in two halves with the
+// products of the first beside the weights of the second (+ 10 %), rows through
+// shared memory into bulk copies at the end (+ 7 %), P beside S for heads of 64 with
+// the next scores early (163 us for 139 at 256 x 196).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

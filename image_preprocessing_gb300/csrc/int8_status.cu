@@ -1,4 +1,4 @@
-// The status word of the int8 product's kernels: bit 0 (kStatusTimeout) after a
+// The status word of the int8 product's and the attention's kernels: bit 0 (kStatusTimeout) after a
 // wait that ran out.  In a file of its own: its address is asked for without
 // loading kernels, the product's or the fused step's (14 ms).
 #include <cuda_runtime.h>

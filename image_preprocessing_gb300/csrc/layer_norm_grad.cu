@@ -5,8 +5,12 @@
 //     dx_c = s (g_c - sum_j g_j / n - u_c s^2 (sum_j g_j u_j) / n) + dres_c
 //     dw_c = sum_rows dy_c u_c s,  db_c = sum_rows dy_c
 //
-// Bound by HBM and, beside it, by the instructions and the two reductions that a
-// row needs one after the other.
+// Bound by HBM and, beside it, by the instructions (56 % of the issue slots with
+// 17 % of the warps) and the two reductions that a row needs one after the other.
+// Measured (of the copy rate): 50176 x 1024 binary16 79 us (0.77), 12544 x 4096
+// bfloat16 96 us (0.63), 50176 x 768 89 us (0.51: a third of the lanes' second packs
+// are empty), 50176 x 511 104 us (0.22: shifted packs, CTAs of one row).  Above 8192
+// columns 1024 threads leave 64 registers to a thread and sums spill.
 #include "row_parts.h"
 
 namespace trfn {

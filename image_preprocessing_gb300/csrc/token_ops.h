@@ -127,7 +127,7 @@ int launch_int8_mid(const MatmulArgs& a);
 double int8_gemm_cycles(long long M, long long N, long long K);
 double int8_mid_cycles(long long M, long long N, long long K);
 
-// The int8 product's status word (int8_status.cu) on device `dev`, the current
+// The int8 product's and the attention's status word (int8_status.cu) on device `dev`, the current
 // one; reading it (as read_device_status, on the current device) copies nothing
 // before the word has been asked for there.
 int product_status_word(int dev, unsigned** word);

@@ -33,9 +33,9 @@
  *     overlap; with different row distances, ranges that cross are refused.
  *   - rows = 0 is no work (a dweight is still written: zeros); cols is at least 1.
  *   - Calls that may run at the same time need workspaces of their own.
- *   - A product whose pipeline waits for more than about a second sets bit 0 of
- *     tr_device_status()'s word; parts of its output are then not written, the
- *     rest is right.
+ *   - A product or an attention whose pipeline waits for more than about a
+ *     second sets bit 0 of tr_device_status()'s word; parts of its output are then
+ *     not written, the rest is right.
  */
 #ifndef TR_TOKEN_OPS_H
 #define TR_TOKEN_OPS_H
@@ -240,8 +240,9 @@ size_t tr_attention_workspace_bytes(long long q_rows, long long sequences, long 
  *                likewise (slots of a cache, filled in part).
  * Sequences may be empty, keys shared by several.  The arrays are read by the
  * GPU: nothing outside q, k and v is read whatever they hold (rows beyond a
- * matrix, or ends before starts, are cut off), and rows of q that belong to
- * two sequences get either's output.  Rows that belong to none are not written.
+ * matrix, or ends before starts, are cut off).  Sequences' queries do not overlap
+ * (rows of q that two of them claim get the output of either, or none).  Rows that
+ * belong to none are not written.
  *   workspace    device, tr_attention_workspace_bytes() bytes for these rows and
  *                sequences or more, 16-byte aligned, not initialised.
  * Scores, maxima, sums and outputs are binary32; in F16 and BF16 a weight p is
@@ -249,7 +250,8 @@ size_t tr_attention_workspace_bytes(long long q_rows, long long sequences, long 
  * reach its output, whatever it holds (infinities and NaN included).  The same
  * call gives the same bits.
  * Fast for F16 and BF16 with dim a multiple of 8 up to 128, up to 64 heads to a
- * key head, and matrices and strides on 16 bytes; a plain kernel takes the rest.
+ * key head, a scale above 0, and matrices and strides on 16 bytes (rows that do
+ * not overlap); a plain kernel takes the rest.
  * TR_ERR_INVALID_ARGUMENT where heads is no multiple of kv_heads or out overlaps
  * another buffer; TR_ERR_NOT_SUPPORTED for dim > TR_MAX_HEAD_DIM, heads >
  * TR_MAX_HEADS, sequences > TR_MAX_SEQUENCES or rows > TR_MAX_ATTENTION_ROWS. */

@@ -796,6 +796,24 @@ def test_attention_of_arrays_that_leave_the_matrices(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=name_of)
+def test_attention_of_repeated_and_interleaved_rows(dtype):
+    """One key row that is repeated (stride 0), and queries, keys, values and outputs as column blocks of one buffer."""
+    p = Problem(4, [70, 9], [70, 9], 2, 2, 64, dtype)
+    row = p.buf.randn(1, 128).to(dtype)
+    p.k = row.expand(79, 128)
+    p.check(p.run(True), True)
+    p.v = row.expand(79, 128)
+    p.check(p.run(False), False)
+    whole = torch.zeros(79, 4 * 128, dtype=dtype, device="cuda")
+    whole[:, :384] = p.buf.randn(79, 384).to(dtype)
+    p.q, p.k, p.v, out = (whole[:, i * 128:(i + 1) * 128] for i in range(4))
+    kept = whole[:, :384].clone()
+    p.check(p.run(True, out=out), True)
+    assert torch.equal(whole[:, :384], kept)
+
+
+@gpu
 def test_attention_of_no_rows_and_no_sequences():
     e = torch.empty(0, 128, device="cuda", dtype=torch.float16)
     before = trfn.tr_launch_count()
