@@ -8,8 +8,7 @@
 // Bound by HBM and, beside it, by the instructions (56 % of the issue slots with
 // 17 % of the warps) and the two reductions that a row needs one after the other.
 // Measured (of the copy rate): 50176 x 1024 binary16 79 us (0.77), 12544 x 4096
-// bfloat16 96 us (0.63), 50176 x 768 89 us (0.51: a third of the lanes' second packs
-// are empty), 50176 x 511 104 us (0.22: shifted packs, CTAs of one row).  Above 8192
+// bfloat16 96 us (0.63), 50176 x 768 82 us (0.56), 50176 x 511 104 us (0.22: shifted packs, CTAs of one row).  Above 8192
 // columns 1024 threads leave 64 registers to a thread and sums spill.
 #include "row_parts.h"
 
@@ -40,17 +39,16 @@ constexpr int kLayerAhead = V == 1 ? 0 : (V == 8 ? 3 : 2) * kLayerRowBytes<V, T,
 // (50176 x 1024: 161 registers against 128).  Rows of 1024 threads have no room for them there.
 template <int T> constexpr bool kSharedWeights = T <= 512;
 
+// CTAs that an SM is to hold, one wave of which is launched (24 values a thread take the registers of two).
+template <int T> constexpr int kGradResident = T == 32 ? 2 : T == 64 ? 6 : T == 128 ? 4 : T == 256 ? 2 : 1;
+
 // T threads take a row, T = 32 eight rows to a CTA at a time, which goes
 // through the matrix with the grid's stride.  A thread's columns are the same
 // in every row (with SHIFT too: the grid and the rows of a CTA are multiples of
-// 8), so it keeps their sums of dweight and dbias in
-// registers, and the CTA writes the sums as one partial row.  Two reductions:
+// 8), so it keeps their sums of dweight and dbias in registers, and the CTA writes the sums as one partial row.  Two reductions:
 // of (h, g), then of ((h - m)^2, g (h - m)).
-// CTAs that an SM is to hold, one wave of which is launched.
-template <int T> constexpr int kGradResident = T == 32 ? 2 : T == 64 ? 6 : T == 128 ? 4 : T == 256 ? 2 : 1;
-
 template <typename E, int V, int T, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kThreads<T>, kGradResident<T>) layer_grad_kernel(const LayerGradParams p) {
+__global__ void __launch_bounds__(kThreads<T>, T == 32 && V * NV > 16 ? 1 : kGradResident<T>) layer_grad_kernel(const LayerGradParams p) {
     constexpr int R = kThreads<T> / T, N = NV * V;   // N values to a thread
     static_assert(N % 2 == 0 && N <= 32, "values are taken in pairs, and have a bit each");
     constexpr int AHEAD = kLayerAhead<V, T, NV>;
@@ -268,6 +266,7 @@ int pick_layer_grad(const LayerGradParams& p, int* parts, cudaStream_t st) {
     const int n = p.cols + (SHIFT ? V - 1 : 0);
     if (n <= 256) return start_layer_grad<E, V, 32, 8, SHIFT>(p, parts, st);
     if (n <= 512) return start_layer_grad<E, V, 32, 16, SHIFT>(p, parts, st);
+    if (n <= 768) return start_layer_grad<E, V, 32, 24, SHIFT>(p, parts, st);
     if (n <= 1024) return start_layer_grad<E, V, 64, 16, SHIFT>(p, parts, st);
     if (n <= 2048) return start_layer_grad<E, V, 128, 16, SHIFT>(p, parts, st);
     if (n <= 4096) return start_layer_grad<E, V, 256, 16, SHIFT>(p, parts, st);
@@ -295,7 +294,7 @@ int type_layer_grad(const LayerGradParams& p, int* parts, cudaStream_t st) {
 int layer_norm_grad_parts(long long rows, long long cols) {
     // by the length alone, so that the workspace is known before the matrices are: off the boundaries the last
     // lengths below each change of threads a row (up to 7 packs' values of them) take the next layout
-    auto threads = [](long long n) { return n <= 512 ? 32 : n <= 1024 ? 64 : n <= 2048 ? 128 : n <= 4096 ? 256 : 512; };
+    auto threads = [](long long n) { return n <= 768 ? 32 : n <= 1024 ? 64 : n <= 2048 ? 128 : n <= 4096 ? 256 : 512; };
     const int a = layer_grad_ctas(rows, threads(cols)), b = layer_grad_ctas(rows, threads(cols + 7));
     return a > b ? a : b;
 }
