@@ -16,7 +16,8 @@
 // thread does that itself, so there is no correction in the usual block.
 //
 // P is rounded to the type of v, half a unit relative to itself, as the products
-// take it; in binary16 the weights are made 2^6 times as large, so that the ones
+// take it, and l is the sum of what they take: where one key has nearly all the
+// weight, its rounding is no error (costs 2 %); in binary16 the weights are made 2^6 times as large, so that the ones
 // below 2^-14 of the largest keep more of their bits.
 //
 // What a row does not see: its weight is an exact zero, but 0 times an infinity is
@@ -32,11 +33,11 @@
 // last is visible, weights some 1500, the products with v and the handing over)
 // is longer than the 2048 cycles that the tensor cores need for both tiles' block
 // at 128 values a head, and twice their time at 64.  Measured: 8192 causal queries,
-// 32 heads of 128 over 8 key heads, bfloat16, 504 us, 1091 TFLOP/s (0.57 of the
+// 32 heads of 128 over 8 key heads, bfloat16, 510 us, 1077 TFLOP/s (0.56 of the
 // measured peak; the tensor pipe active 53 % of the cycles); 16 packed prompts of up to
-// 4096 304 us (0.41); 256 x 196, 12 heads of 64, binary16, 146 us (0.31 of the copy
+// 4096 306 us (0.41); 256 x 196, 12 heads of 64, binary16, 147 us (0.31 of the copy
 // rate); one token for each of 32 sequences over 42,000 keys in all 58 us (0.44 of
-// the copy rate; even lengths of 4096 110 us, 0.72).
+// the copy rate; even lengths of 4096 113 us, 0.70).
 //
 // Shared memory leaves L1 a few KB, so whatever a thread keeps in local memory
 // comes from L2 each time: a kernel that spilled a few hundred bytes took five
@@ -243,6 +244,14 @@ template <> __device__ __forceinline__ uint32_t not_finite2<__nv_bfloat16>(uint3
 __device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
 __device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Adds both rounded values to binary32 sums.
+template <typename E> __device__ __forceinline__ void add_rounded(uint32_t w, float& lo, float& hi);
+template <> __device__ __forceinline__ void add_rounded<__half>(uint32_t w, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.f16 %0, a, %0;\n\tadd.f32.f16 %1, b, %1;\n\t}" : "+f"(lo), "+f"(hi) : "r"(w));
+}
+template <> __device__ __forceinline__ void add_rounded<__nv_bfloat16>(uint32_t w, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.bf16 %0, a, %0;\n\tadd.f32.bf16 %1, b, %1;\n\t}" : "+f"(lo), "+f"(hi) : "r"(w));
+}
 template <typename E> __device__ __forceinline__ E from_value(float v);
 template <> __device__ __forceinline__ __half from_value<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_value<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
@@ -753,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     }
                     const float off = ms == -INFINITY ? 0.0f : ms;   // nothing seen yet: weights 0
                     const Two scale2 = two(p.scale, p.scale), off2 = two(-off, -off);
-                    Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // of the weights as the products take them
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (g * 32 >= cols) continue;
@@ -762,13 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         for (int i = 0; i < 32; i += 2) {
                             const float2 y = apart(fma_two(two(__uint_as_float(x[g * 32 + i]), __uint_as_float(x[g * 32 + i + 1])), scale2, off2));
                             const float a = power2(y.x), b = power2(y.y);
-                            sum[i / 2 & 1] = add_two(sum[i / 2 & 1], two(a, b));
                             w[i / 2] = pack2<E>(a, b);
+                            add_rounded<E>(w[i / 2], sum[i & 2], sum[(i & 2) + 1]);
                         }
                         tmem_store16(tm + tile * kKeys + g * 16, w);
                     }
-                    const float2 all = apart(add_two(sum[0], sum[1]));
-                    l += all.x + all.y;
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_stored();
                 }
                 tmem_fence_before();

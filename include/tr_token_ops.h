@@ -246,7 +246,7 @@ size_t tr_attention_workspace_bytes(long long q_rows, long long sequences, long 
  *   workspace    device, tr_attention_workspace_bytes() bytes for these rows and
  *                sequences or more, 16-byte aligned, not initialised.
  * Scores, maxima, sums and outputs are binary32; in F16 and BF16 a weight p is
- * rounded to dtype for the product with v.  What a query does not see does not
+ * rounded to dtype for the product with v and for the sum.  What a query does not see does not
  * reach its output, whatever it holds (infinities and NaN included).  The same
  * call gives the same bits.
  * Fast for F16 and BF16 with dim a multiple of 8 up to 128, up to 64 heads to a

@@ -706,6 +706,27 @@ def test_attention_of_even_and_sharp_scores(sharp, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", SHORT, ids=name_of)
+def test_attention_of_one_key_that_has_all_the_weight(dtype):
+    """A maximum that grows by less than what makes the kernel start over (2^8) leaves the largest weight above 1 and
+    rounded; the sum takes the same rounded weight, so the output is nearly that key's value within the output's
+    own rounding: the rounding of its weight reaches it only through the other key's share, e^-gap."""
+    p = Problem(6, [64], [256], 1, 1, 64, dtype)
+    p.q[:] = 0
+    p.k[:] = 0
+    p.q[:, 0] = 8.0           # scores are the keys' first values
+    p.k[:, 0] = -60.0
+    p.k[0, 0] = -20.0         # the first block's maximum
+    for top in (-15.9, -15.1, -14.9, -14.7):
+        p.k[200, 0] = top
+        p.check(p.run(False), False)
+        gap = math.exp(float(p.k[200, 0].double() + 20))
+        v = p.v.double()
+        want = (v[200] * gap + v[0]) / (gap + 1)
+        near(p.out, want.expand(64, 64), v.abs().max() * (4 * UNIT[dtype] / gap + 2.0 ** -18), dtype)
+
+
+@gpu
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.5, 1e-30])
 def test_attention_scales(scale):
     for dtype in TYPES:
