@@ -26,7 +26,7 @@ namespace attention {
 constexpr int kRows = 128, kKeys = 128;   // of a tile, of a block
 constexpr int kItemCost = 2;
 
-// a / b and a % b, by the narrow division where that does.
+// a / b, by the narrow division where that does.
 TRFN_BOTH unsigned long long quotient(unsigned long long a, unsigned long long b) {
     return (a | b) >> 32 ? a / b : (unsigned)a / (unsigned)b;
 }

@@ -5,10 +5,8 @@
 // is two tiles of 128 rows (queries x heads of one key head) over blocks of 128
 // keys.  Warps: one copies (TMA: queries, then keys and values through a ring of
 // stages) and says what comes next; one issues the products; one makes values that
-// a row does not see harmless; eight for each tile do the softmax, two threads a row
-// (64 scores are what a thread can hold, and four warps to a scheduler hide one
-// another's waits: 128 scores in one thread of four warps took twice as long).
-//     S = Q K^T into TMEM; a row's threads read it, keep maximum and sum, writes
+// a row does not see harmless; four for each tile do the softmax, a thread a row.
+//     S = Q K^T into TMEM; a row's thread reads it, keeps maximum and sum, writes
 //     P = 2^(x - m) in 16 bits over S; O += P V in TMEM, P read from there.
 // The tiles take turns: the tensor cores multiply for one while the other's
 // weights are made.  O is multiplied by 2^(m_old - m_new) only where the maximum
@@ -17,8 +15,9 @@
 //
 // P is rounded to the type of v, half a unit relative to itself, as the products
 // take it, and l is the sum of what they take: where one key has nearly all the
-// weight, its rounding is no error (costs 2 %); in binary16 the weights are made 2^6 times as large, so that the ones
-// below 2^-14 of the largest keep more of their bits.
+// weight, its rounding is no error (costs 2 %).  In binary16 the weights are made
+// 2^6 times as large, so that the ones below 2^-14 of the largest keep more of
+// their bits.
 //
 // What a row does not see: its weight is an exact zero, but 0 times an infinity is
 // not.  In blocks that some row does not see whole, values that are not finite are
@@ -419,8 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    auto s_at = [&](int t) { return tmem + t * kKeys; };
-    auto o_at = [&](int t) { return tmem + 2 * kKeys + t * D; };
     auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait_here(bar, parity, &given_up, p.status); };
     auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait_here(bar, parity, &given_up, p.status)) != 0; };
     // Whether the piece with this number is there and not the end; and that the warp is done with it.
